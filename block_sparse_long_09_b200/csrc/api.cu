@@ -163,6 +163,48 @@ const __nv_bfloat16 *bf(const qsa_bf16 *p) { return reinterpret_cast<const __nv_
 __nv_bfloat16 *bf(qsa_bf16 *p) { return reinterpret_cast<__nv_bfloat16 *>(p); }
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// do two ranges of memory share a byte (a NULL range shares none)
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes)
+{
+    if (a == nullptr || b == nullptr) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
+// the pool arguments that the paged-cache calls share
+qsa_status check_pool(const qsa_config *c, int32_t format, const void *k_pages, const void *v_pages,
+                      const uint8_t *k_scales, const uint8_t *v_scales, int64_t num_pages, int32_t page_size,
+                      const int32_t *block_table, int32_t max_pages)
+{
+    if (format != QSA_CACHE_BF16 && format != QSA_CACHE_E4M3) return QSA_ERR_INVALID_ARG;
+    if (num_pages <= 0 || page_size <= 0 || max_pages <= 0 || block_table == nullptr) return QSA_ERR_INVALID_ARG;
+    if (k_pages == nullptr || v_pages == nullptr || !al16(k_pages) || !al16(v_pages)) return QSA_ERR_INVALID_ARG;
+    if (format == QSA_CACHE_E4M3 && (k_scales == nullptr || v_scales == nullptr)) return QSA_ERR_INVALID_ARG;
+    if (num_pages >= ((int64_t)1 << 31) || num_pages * page_size * c->n_heads_kv >= ((int64_t)1 << 31))
+        return QSA_ERR_UNSUPPORTED;
+    return QSA_OK;
+}
+
+// does a range overlap one of the pool's four arrays
+bool in_pool(const qsa_config *c, const void *p, int64_t bytes, int32_t format, const void *k_pages,
+             const void *v_pages, const uint8_t *k_scales, const uint8_t *v_scales, int64_t num_pages,
+             int32_t page_size)
+{
+    const int64_t rows = num_pages * page_size * c->n_heads_kv;
+    const int64_t codes = rows * c->head_dim * (format == QSA_CACHE_E4M3 ? 1 : 2);
+    if (overlap(p, bytes, k_pages, codes) || overlap(p, bytes, v_pages, codes)) return true;
+    return format == QSA_CACHE_E4M3 && (overlap(p, bytes, k_scales, rows) || overlap(p, bytes, v_scales, rows));
+}
+
+qsa::CachePool pool_of(int32_t format, const void *k_pages, const void *v_pages, const uint8_t *k_scales,
+                       const uint8_t *v_scales, int64_t num_pages, int32_t page_size, const int32_t *block_table,
+                       int32_t max_pages)
+{
+    return qsa::CachePool{const_cast<void *>(k_pages), const_cast<void *>(v_pages), const_cast<uint8_t *>(k_scales),
+                          const_cast<uint8_t *>(v_scales), format == QSA_CACHE_E4M3 ? 1 : 0, num_pages, page_size,
+                          block_table, max_pages};
+}
+
 }  // namespace
 
 extern "C" {
@@ -211,6 +253,7 @@ size_t qsa_workspace_size(const qsa_config *cfg, int32_t op, int32_t batch, int6
         return batch < 2 * kMaxEvenCtas ? even_workspace_bytes(batch, kMaxEvenCtas) : 0;
     if (op == QSA_OP_DECODE_PAGED) return even_workspace_bytes(batch, kMaxEvenCtas);
     if (op == QSA_OP_DECODE_MTP) return mtp_workspace_bytes(batch, cfg->budget_blocks);
+    if (op == QSA_OP_CHUNK_PAGED) return chunk_workspace_bytes(batch, rows);
     if (op == QSA_OP_INDEX_SELECT_PAGED)  // one score row per sequence
         return (size_t)batch * (max_len_k > 0 ? ((max_len_k - 1) / cfg->r + 3) / 4 * 4 + 4 : 4) * sizeof(float);
     if (op == QSA_OP_PREFILL) {
@@ -624,6 +667,117 @@ qsa_status qsa_dense_attn_prefill(const qsa_config *cfg, const qsa_bf16 *q, cons
     DenseArgs a{bf(q), bf(k), bf(v), cu_seqlens_q, cu_seqlens_k, batch, total_q, total_k, max_len_q, bf(o), lse,
                 cfg->softmax_scale};
     return cuda_status(launch_dense_attn(a, s));
+}
+
+qsa_status qsa_cache_write_paged(const qsa_config *cfg, const qsa_bf16 *k, const qsa_bf16 *v,
+                                 const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int32_t batch,
+                                 int64_t total_q, int32_t format, void *k_pages, void *v_pages, uint8_t *k_scales,
+                                 uint8_t *v_scales, int64_t num_pages, int32_t page_size, const int32_t *block_table,
+                                 int32_t max_pages, void *stream)
+{
+    const qsa::NvtxRange nvtx_range("qsa_cache_write_paged");
+    qsa_status st = check_config(cfg);
+    if (st != QSA_OK) return st;
+    if (batch <= 0 || total_q < 0 || cu_seqlens_q == nullptr || cu_seqlens_k == nullptr) return QSA_ERR_INVALID_ARG;
+    st = check_pool(cfg, format, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, block_table, max_pages);
+    if (st != QSA_OK) return st;
+    if (total_q == 0) return QSA_OK;
+    if (k == nullptr || v == nullptr || !al16(k) || !al16(v)) return QSA_ERR_INVALID_ARG;
+    for (const qsa_bf16 *p : {k, v})
+        if (in_pool(cfg, p, total_q * cfg->n_heads_kv * cfg->head_dim * 2, format, k_pages, v_pages, k_scales,
+                    v_scales, num_pages, page_size))
+            return QSA_ERR_INVALID_ARG;
+    return cuda_status(launch_cache_write(pool_of(format, k_pages, v_pages, k_scales, v_scales, num_pages, page_size,
+                                                  block_table, max_pages),
+                                          bf(k), bf(v), cu_seqlens_q, cu_seqlens_k, batch, total_q,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+qsa_status qsa_cache_read_paged(const qsa_config *cfg, int32_t format, const void *k_pages, const void *v_pages,
+                                const uint8_t *k_scales, const uint8_t *v_scales, int64_t num_pages,
+                                int32_t page_size, const int32_t *block_table, int32_t max_pages,
+                                const int32_t *cu_seqlens_k, const int32_t *tok_begin, const int32_t *cu_out,
+                                int32_t batch, int64_t total_out, qsa_bf16 *k_out, qsa_bf16 *v_out, void *stream)
+{
+    const qsa::NvtxRange nvtx_range("qsa_cache_read_paged");
+    qsa_status st = check_config(cfg);
+    if (st != QSA_OK) return st;
+    if (batch <= 0 || total_out < 0 || cu_seqlens_k == nullptr || cu_out == nullptr) return QSA_ERR_INVALID_ARG;
+    st = check_pool(cfg, format, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, block_table, max_pages);
+    if (st != QSA_OK) return st;
+    if (total_out == 0) return QSA_OK;
+    if (k_out == nullptr || v_out == nullptr || !al16(k_out) || !al16(v_out)) return QSA_ERR_INVALID_ARG;
+    const int64_t out_bytes = total_out * cfg->n_heads_kv * cfg->head_dim * 2;
+    for (const qsa_bf16 *p : {k_out, v_out})
+        if (in_pool(cfg, p, out_bytes, format, k_pages, v_pages, k_scales, v_scales, num_pages, page_size))
+            return QSA_ERR_INVALID_ARG;
+    if (overlap(k_out, out_bytes, v_out, out_bytes)) return QSA_ERR_INVALID_ARG;
+    return cuda_status(launch_cache_read(pool_of(format, k_pages, v_pages, k_scales, v_scales, num_pages, page_size,
+                                                 block_table, max_pages),
+                                         cu_seqlens_k, tok_begin, cu_out, batch, total_out, bf(k_out), bf(v_out),
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+qsa_status qsa_chunk_attn_paged(const qsa_config *cfg, const qsa_bf16 *q, int32_t format, const void *k_pages,
+                                const void *v_pages, const uint8_t *k_scales, const uint8_t *v_scales,
+                                int64_t num_pages, int32_t page_size, const int32_t *block_table, int32_t max_pages,
+                                const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int32_t batch,
+                                int64_t total_q, int32_t max_len_q, int32_t window, int32_t sinks, qsa_bf16 *o,
+                                float *lse, void *ws, size_t ws_bytes, void *stream)
+{
+    const qsa::NvtxRange nvtx_range("qsa_chunk_attn_paged");
+    qsa_status st = check_config(cfg);
+    if (st != QSA_OK) return st;
+    if (batch <= 0 || total_q < 0 || max_len_q < 0 || window < 0 || sinks < 0 || cu_seqlens_q == nullptr ||
+        cu_seqlens_k == nullptr)
+        return QSA_ERR_INVALID_ARG;
+    st = check_pool(cfg, format, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, block_table, max_pages);
+    if (st != QSA_OK) return st;
+    if (total_q == 0) return QSA_OK;
+    if (total_q >= ((int64_t)1 << 28)) return QSA_ERR_UNSUPPORTED;
+    if (q == nullptr || o == nullptr || !al16(q) || !al16(o)) return QSA_ERR_INVALID_ARG;
+    if (ws == nullptr || ws_bytes < chunk_workspace_bytes(batch, total_q)) return QSA_ERR_WORKSPACE_TOO_SMALL;
+    if (!al16(ws)) return QSA_ERR_INVALID_ARG;
+    const int64_t q_bytes = total_q * cfg->n_heads_q * cfg->head_dim * 2;
+    if (overlap(q, q_bytes, o, q_bytes)) return QSA_ERR_INVALID_ARG;
+    for (const void *p : {static_cast<const void *>(o), static_cast<const void *>(lse)})
+        if (in_pool(cfg, p, p == o ? q_bytes : total_q * cfg->n_heads_q * 4, format, k_pages, v_pages, k_scales,
+                    v_scales, num_pages, page_size))
+            return QSA_ERR_INVALID_ARG;
+    ChunkArgs a{bf(q), pool_of(format, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, block_table, max_pages),
+                cu_seqlens_q, cu_seqlens_k, batch, total_q, max_len_q, window, sinks, cfg->softmax_scale, bf(o), lse,
+                static_cast<float *>(ws)};
+    return cuda_status(launch_chunk_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
+qsa_status qsa_rope_axes(const qsa_config *cfg, const qsa_bf16 *q, const qsa_bf16 *k, const int32_t *positions,
+                         int64_t total, int32_t s0, int32_t s1, int32_t s2, uint32_t flags, qsa_bf16 *q_out,
+                         qsa_bf16 *k_out, void *stream)
+{
+    const qsa::NvtxRange nvtx_range("qsa_rope_axes");
+    qsa_status st = check_config(cfg);
+    if (st != QSA_OK) return st;
+    if (total < 0 || s0 < 0 || s1 < 0 || s2 < 0 || (flags & ~(QSA_ROPE_INTERLEAVED | QSA_ROPE_INVERSE)) != 0)
+        return QSA_ERR_INVALID_ARG;
+    const int64_t h = (int64_t)s0 + s1 + s2;
+    if (h < 1 || 2 * h > cfg->head_dim || !(cfg->rope_base > 1.f) || !(cfg->rope_base < 3.0e38f))
+        return QSA_ERR_INVALID_ARG;
+    if ((flags & QSA_ROPE_INTERLEAVED) != 0 &&
+        ((s1 > 0 && 3 * (s1 - 1) + 1 >= h) || (s2 > 0 && 3 * (s2 - 1) + 2 >= h)))
+        return QSA_ERR_INVALID_ARG;
+    if ((q == nullptr) != (q_out == nullptr) || (k == nullptr) != (k_out == nullptr)) return QSA_ERR_INVALID_ARG;
+    if (!al16(q) || !al16(k) || !al16(q_out) || !al16(k_out)) return QSA_ERR_INVALID_ARG;
+    if (total == 0 || (q == nullptr && k == nullptr)) return QSA_OK;
+    if (positions == nullptr) return QSA_ERR_INVALID_ARG;
+    // a row is rotated in place or into other memory: no other overlap
+    const int64_t q_bytes = total * cfg->n_heads_q * cfg->head_dim * 2, k_bytes = total * cfg->n_heads_kv * cfg->head_dim * 2;
+    if ((q != q_out && overlap(q, q_bytes, q_out, q_bytes)) || (k != k_out && overlap(k, k_bytes, k_out, k_bytes)) ||
+        overlap(q, q_bytes, k_out, k_bytes) || overlap(k, k_bytes, q_out, q_bytes) ||
+        overlap(q_out, q_bytes, k_out, k_bytes))
+        return QSA_ERR_INVALID_ARG;
+    return cuda_status(launch_rope_axes(bf(q), bf(k), positions, total, s0, s1, s2, cfg->rope_base,
+                                        (flags & QSA_ROPE_INTERLEAVED) != 0, (flags & QSA_ROPE_INVERSE) != 0,
+                                        bf(q_out), bf(k_out), static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -285,6 +285,53 @@ struct DenseArgs {
 };
 cudaError_t launch_dense_attn(const DenseArgs &a, cudaStream_t stream);
 
+// A paged K/V pool in one of its two formats (cache.cu): rows of 2 KV heads x 256 values,
+// bf16, or e4m3 codes with one power-of-two scale byte per (row, KV head).
+struct CachePool {
+    void *k, *v;                    // [num_pages * page_size, 2, 256]
+    uint8_t *k_scales, *v_scales;   // [num_pages * page_size, 2], e4m3 only
+    int fp8;
+    int64_t num_pages;
+    int page_size;
+    const int32_t *table;           // [batch, max_pages]
+    int max_pages;
+};
+
+// the scale 2^(byte - 127) of an e4m3 row; 255 stands for a row with a non-finite value
+__device__ __forceinline__ float scale_of_byte(uint32_t byte)
+{
+    return __uint_as_float(byte == 255u ? 0x7FC00000u : (byte == 0u ? 0x00400000u : byte << 23));
+}
+
+cudaError_t launch_cache_write(const CachePool &c, const __nv_bfloat16 *k, const __nv_bfloat16 *v, const int32_t *cu_q,
+                               const int32_t *cu_k, int batch, int64_t total_q, cudaStream_t stream);
+cudaError_t launch_cache_read(const CachePool &c, const int32_t *cu_k, const int32_t *tok_begin, const int32_t *cu_out,
+                              int batch, int64_t total_out, __nv_bfloat16 *k_out, __nv_bfloat16 *v_out,
+                              cudaStream_t stream);
+
+// rotary positions with three axes, and their gradient (rope_axes.cu)
+cudaError_t launch_rope_axes(const __nv_bfloat16 *q, const __nv_bfloat16 *k, const int32_t *pos, int64_t total, int s0,
+                             int s1, int s2, float base, bool interleaved, bool inverse, __nv_bfloat16 *q_out,
+                             __nv_bfloat16 *k_out, cudaStream_t stream);
+
+// Attention of the new tokens of every sequence over its paged cache (attn_chunk.cu)
+struct ChunkArgs {
+    const __nv_bfloat16 *q;         // [total_q, 24, 256]
+    CachePool pool;
+    const int32_t *cu_q, *cu_k;
+    int batch;
+    int64_t total_q;
+    int64_t max_len_q;
+    int64_t window;                 // 0: every earlier token is visible
+    int64_t sinks;                  // first tokens that a window leaves visible
+    float scale;
+    __nv_bfloat16 *o;
+    float *lse;
+    float *ws;
+};
+size_t chunk_workspace_bytes(int batch, int64_t total_q);
+cudaError_t launch_chunk_attn(const ChunkArgs &a, cudaStream_t stream);
+
 // tensor-map creation (host), defined in api.cu
 bool make_tmap_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer,
                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);

@@ -100,6 +100,15 @@ typedef struct qsa_config {
 #define QSA_OP_INDEX_SELECT 7 /* qsa_index_select */
 #define QSA_OP_INDEX_SELECT_PAGED 8 /* qsa_index_select_paged */
 #define QSA_OP_DECODE_MTP 9 /* qsa_sparse_attn_decode_mtp */
+#define QSA_OP_CHUNK_PAGED 10 /* qsa_chunk_attn_paged */
+
+/* formats of a paged K/V pool (qsa_cache_write_paged) */
+#define QSA_CACHE_BF16 0
+#define QSA_CACHE_E4M3 1
+
+/* flags of qsa_rope_axes */
+#define QSA_ROPE_INTERLEAVED 0x1u /* the axes alternate from pair to pair */
+#define QSA_ROPE_INVERSE 0x2u     /* rotate by the negative angle: the gradient */
 
 /* Fill *cfg with the model's values (r 4, k 512, 24/2/256, 4/128, scale 1/16,
  * eps 1e-6, flags 0, kv_chunk_blocks 0, rope_dims 64, rope_base 10000).  Host only. */
@@ -463,6 +472,108 @@ qsa_status qsa_dense_attn_prefill(const qsa_config *cfg, const qsa_bf16 *q, cons
                                   const int32_t *cu_seqlens_k, int32_t batch, int64_t total_q,
                                   int64_t total_k, int32_t max_len_q, int64_t max_len_k,
                                   qsa_bf16 *o, float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The paged K/V cache: writing new tokens, reading a range back, and attention of new
+ * tokens over it.  The reading notes name a paged GQA cache as the dense baseline of their
+ * measurements ("结果 2"); they give no cache format, no window and no image positions, so the
+ * calls below follow their own definitions.  Pool and block table are those of
+ * qsa_sparse_attn_decode_paged:
+ *   k_pages, v_pages  [num_pages, page_size, n_heads_kv, head_dim], 16-byte aligned, in one
+ *                     of two formats (the same for K and V):
+ *       QSA_CACHE_BF16  the values
+ *       QSA_CACHE_E4M3  8-bit codes (4 exponent, 3 mantissa bits, largest 448) with one scale
+ *                       byte per (token, KV head):  value = code * 2^(byte - 127)
+ *   k_scales, v_scales [num_pages, page_size, n_heads_kv] uint8 (E4M3; ignored for BF16)
+ *   block_table       [batch, max_pages] int32: page j of sequence s holds its tokens
+ *                     [j page_size, (j + 1) page_size)
+ *   page_size >= 1 (any; the other paged calls want a multiple of r),
+ *   num_pages * page_size * n_heads_kv < 2^31 (QSA_ERR_UNSUPPORTED otherwise).
+ * New tokens are packed by cu_seqlens_q; token i of sequence s sits at position
+ * t = (L_k,s - L_q,s) + (i - cu_seqlens_q[s]), L_k,s counting the new tokens.  Rows from
+ * cu_seqlens_q[batch] on (padding of a captured batch) are neither read for a result nor
+ * written.  All three calls take any mix of lengths, zero included, from the device arrays, so
+ * a captured call replays on other lengths.
+ *
+ * qsa_cache_write_paged: K and V rows of the new tokens into the pool.  E4M3: per (token,
+ * head) the byte is e + 127 with the smallest e >= -127 such that max|x| <= 448 * 2^e, and
+ * code = x * 2^-e rounded to nearest even: each value is off by at most 2^-4 of itself
+ * (below 2^(e-6), where codes are subnormal, by at most 2^(e-10)).  A row that holds an
+ * infinity or a NaN gets byte 255 and zero codes and reads back as NaN.
+ *   k, v   [total_q, n_heads_kv, head_dim] bf16, 16-byte aligned, not overlapping the pool
+ * A token without a page in the table, or at a negative position (L_q,s > L_k,s), is skipped
+ * and flagged QSA_ERR_DEVICE_CHECK.  Two tokens of one call must not map to the same pool row
+ * (their order is undefined).
+ */
+qsa_status qsa_cache_write_paged(const qsa_config *cfg, const qsa_bf16 *k, const qsa_bf16 *v,
+                                 const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int32_t batch,
+                                 int64_t total_q, int32_t format, void *k_pages, void *v_pages, uint8_t *k_scales,
+                                 uint8_t *v_scales, int64_t num_pages, int32_t page_size, const int32_t *block_table,
+                                 int32_t max_pages, void *stream);
+
+/*
+ * qsa_cache_read_paged: a range of tokens of every sequence as packed bf16 rows (for the
+ * packed calls, e.g. qsa_sparse_attn_prefill behind a cached prefix): row i of sequence s is
+ * its token tok_begin[s] + (i - cu_out[s]).  Exact: a power-of-two scale times a code is a
+ * bf16 value (one below 2^-126 may round).
+ *   cu_seqlens_k [batch + 1] int32: the lengths L_k,s;  tok_begin [batch] int32 or NULL (0)
+ *   cu_out       [batch + 1] int32: prefix sums of the tokens read per sequence
+ *   total_out    host: rows of k_out and v_out;  k_out, v_out [total_out, n_heads_kv, head_dim]
+ * A token outside 0 .. L_k,s - 1, or without a page, gives zeros and flags
+ * QSA_ERR_DEVICE_CHECK.
+ */
+qsa_status qsa_cache_read_paged(const qsa_config *cfg, int32_t format, const void *k_pages, const void *v_pages,
+                                const uint8_t *k_scales, const uint8_t *v_scales, int64_t num_pages,
+                                int32_t page_size, const int32_t *block_table, int32_t max_pages,
+                                const int32_t *cu_seqlens_k, const int32_t *tok_begin, const int32_t *cu_out,
+                                int32_t batch, int64_t total_out, qsa_bf16 *k_out, qsa_bf16 *v_out, void *stream);
+
+/*
+ * qsa_chunk_attn_paged: dense attention of every sequence's new tokens (one decoded token, a
+ * few drafted ones, a chunk of a prompt) over its paged cache, which holds them already:
+ *   o[t, h] = sum_j softmax_j(scale * <q[t, h], k[j, g]>) v[j, g]
+ * over j <= t with, when window > 0, t - j < window or j < sinks (a sliding window beside a
+ * few first tokens that stay visible); window = 0: no window, sinks is ignored.
+ *   q    [total_q, n_heads_q, head_dim] bf16, 16-byte aligned, and so o
+ *   lse  [total_q, n_heads_q] fp32 natural log-sum-exp of the scaled logits, or NULL
+ *   max_len_q host: a bound of every L_q,s (chooses the kernel; the result does not depend
+ *        on it beyond rounding)
+ * fp32 softmax and accumulation, probabilities and output rounded to bf16.  E4M3 codes enter
+ * the products unrounded.  A row without a visible key (a negative position, an empty cache)
+ * gets o = 0, lse = -inf.  Cache memory at positions behind a sequence's end and pages wholly
+ * outside the window are not read into any result and may hold anything; their table
+ * entries are not looked up.  A visible position without a page counts as a zero key and
+ * value and flags QSA_ERR_DEVICE_CHECK.  In a BF16 pool a non-finite V value may reach rows of
+ * neighbouring tokens that do not see it.
+ * Workspace: qsa_workspace_size(cfg, QSA_OP_CHUNK_PAGED, batch, total_q, 0) bytes, 16-byte
+ * aligned; calls that may overlap on the GPU need one each.  No attention between two calls
+ * is kept in it.
+ */
+qsa_status qsa_chunk_attn_paged(const qsa_config *cfg, const qsa_bf16 *q, int32_t format, const void *k_pages,
+                                const void *v_pages, const uint8_t *k_scales, const uint8_t *v_scales,
+                                int64_t num_pages, int32_t page_size, const int32_t *block_table, int32_t max_pages,
+                                const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int32_t batch,
+                                int64_t total_q, int32_t max_len_q, int32_t window, int32_t sinks, qsa_bf16 *o,
+                                float *lse, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * qsa_rope_axes: rotary positions with three axes (time, height, width: a text token has the
+ * same position on all three, an image or video patch its own) for the attention's q and k,
+ * before they are cached.  With h = s0 + s1 + s2 pairs per head (1 <= h <= head_dim / 2), pair
+ * i is the dims (i, i + h) and rotates by positions[axis(i)][row] * rope_base^(-i / h) (cfg->
+ * rope_base); dims from 2 h on are copied.  axis(i) is 0 for the first s0 pairs, 1 for the
+ * next s1, 2 for the last s2; with QSA_ROPE_INTERLEAVED axis 1 has the pairs 1, 4, 7, ...
+ * (s1 of them), axis 2 the pairs 2, 5, 8, ... (s2), axis 0 the rest (all of them must lie
+ * below h: QSA_ERR_INVALID_ARG otherwise).  QSA_ROPE_INVERSE rotates by the negative angle: the
+ * gradient with respect to the input, given that of the output.
+ *   positions [3, total] int32 (negative ones too);  total host: rows
+ *   q, q_out [total, n_heads_q, head_dim] bf16, 16-byte aligned; q_out == q rotates in place;
+ *   k, k_out [total, n_heads_kv, head_dim] likewise; q or k may be NULL (with its output)
+ * Angles in fp64, products in fp32, one rounding to bf16.
+ */
+qsa_status qsa_rope_axes(const qsa_config *cfg, const qsa_bf16 *q, const qsa_bf16 *k, const int32_t *positions,
+                         int64_t total, int32_t s0, int32_t s1, int32_t s2, uint32_t flags, qsa_bf16 *q_out,
+                         qsa_bf16 *k_out, void *stream);
 
 /* Workspace bytes an op needs (0 = none).  rows = query rows of the call,
  * max_len_k = longest key sequence.  Host only, no CUDA calls. */
