@@ -1,0 +1,797 @@
+// attn_chunk_tc.cu -- attention of the new tokens of every sequence over its paged cache,
+// tensor-core kernel: up to 21 new tokens (252 rows of a KV head's queries) per item.
+//
+//   S = Q K^T,  P = exp2(c2 S - m),  O = P V,  o = O / rowsum(P)       c2 = scale log2(e)
+//
+// A pair of CTAs (cta_group::2) works on an item: 256 rows, 128 per CTA, against tiles of 128 keys.
+// The twelve heads of a KV head fill the rows, so that every key read serves 252 rows and the
+// causal edge of a chunk wastes 21 keys at most; each CTA holds half of every K tile (64 keys)
+// and of every V tile (128 of the 256 dims), so that a pair reads each key once.
+//   S: M 256 N 128 K 256, Q and K from shared memory, two buffers of 128 TMEM columns
+//   O: M 256 N 256 K 128, P from TMEM (the first half of its S buffer, as bf16), V from shared
+//      memory; 256 TMEM columns, so the 512 columns of an SM are full
+// S(i + 1) is issued before O += P(i) V(i): the tensor cores run it while the softmax of
+// tile i is done, whose 128 exponentials per row (1024 cycles of an SM's exp2 units)
+// take half of the 2048 cycles of the tile's two products.
+//   warp 0       Q, once per item (TMA)
+//   warp 1       CTA 0: issues the products of both CTAs; CTA 1: passes on to CTA 0 that its Q is there
+//   warps 2, 3   (bf16 pools) K and V half tiles into a ring of five 32 KB slots, by 16-byte
+//                asynchronous copies: pages of any size, and zeros for keys that no row of the
+//                item sees.  (TMA gathers of four rows by index took 75 cycles per 512 bytes.)
+//   warps 4..7   softmax, a thread per row; running maxima move (and O is rescaled) only when a
+//                row's maximum grows by more than 2^8
+//   warps 8..11  (e4m3 pools) codes to bf16 in registers, exactly: the 7 low bits moved to the
+//                top of a bf16, times 2^120 times the row's scale; then to one of four slots
+// Work is shared out and cut items are merged as chunk_common.cuh describes.  Every wait is bounded.
+#include <mutex>
+
+#include "chunk_common.cuh"
+
+namespace qsa {
+
+namespace {
+
+constexpr int kTcTok = 21, kTcRows = kTcTok * kGrp, kTcKeys = 128;
+constexpr int kTcSlot = 32768, kTcMaxStages = 5;
+constexpr int kTcQ = 128 * kD * 2;
+constexpr int kTcQChunk = 128 * 128, kTcKChunk = 64 * 128, kTcVChunk = 128 * 128;
+constexpr uint32_t kTcO = 256, kTcCols = 512;
+constexpr float kTcRescale = 8.f;
+constexpr int64_t kTcMaxPairs = 80;
+
+struct TcShared {
+    uint64_t kv_full[kTcMaxStages], kv_empty[kTcMaxStages];
+    uint64_t q_full, q_peer, q_empty;
+    uint64_t s_full[2], p_full[2];
+    uint64_t pv_done, o_full, o_empty;
+    uint32_t tmem_base;
+    int abort_flag;
+    int64_t scan[12];
+    ChunkShare share;
+};
+
+struct TcTable {  // e4m3: pool rows and scale bytes of a tile's keys (a ring of three tiles)
+    int32_t row[3][kTcKeys];
+    uint8_t ks[3][kTcKeys], vs[3][kTcKeys];
+};
+
+template <bool kFp8>
+struct TcCfg {
+    static constexpr int kThreads = kFp8 ? 384 : 256;
+    static constexpr int kStages = kFp8 ? 4 : 5;
+    static constexpr int kLoaders = kFp8 ? 4 : 2;  // warps of a CTA that fill the slots
+    static constexpr int kOffRing = kTcQ;
+    static constexpr int kOffTable = kOffRing + kStages * kTcSlot;
+    static constexpr int kOffShared = kOffTable + (kFp8 ? (int)sizeof(TcTable) : 0);
+    static constexpr int kSmem = kOffShared + (int)sizeof(TcShared) + 1024;
+    static_assert(kSmem <= 232448, "shared memory of one CTA");
+};
+
+__device__ __forceinline__ uint32_t cta_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// arrive on the barrier at the same place in CTA 0 of the pair
+__device__ __forceinline__ void arrive_leader(uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .b32 r;\n\t"
+        "mapa.shared::cluster.u32 r, %0, 0;\n\t"
+        "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}"
+        ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    return ok != 0;
+}
+
+// bounded wait for arrivals from either CTA of the pair
+static __device__ __noinline__ bool wait_pair_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+        if (try_wait_cluster(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 > QSA_WAIT_LIMIT_NS) {
+            set_device_status(QSA_ERR_TIMEOUT);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ bool wait_pair(uint64_t *bar, uint32_t parity, volatile int *abort_flag)
+{
+    if (try_wait_cluster(bar, parity)) return true;
+    return wait_pair_slow(bar, parity, abort_flag);
+}
+
+// 16 bytes global -> shared, zeros unless `have`
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool have)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
+}
+
+// D (+)= A B^T over the pair, A from shared memory or from TMEM
+__device__ __forceinline__ void mma2_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+// arrive on the barrier of both CTAs once this thread's tcgen05 operations have completed
+__device__ __forceinline__ void commit_both(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
+        " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16,"
+        " %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+          "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
+          "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The items of a share, in order: every role walks the same list.
+struct TcWalk {
+    int64_t at, te, slot, first;
+    // the current item
+    ChunkGroup g;
+    int hd, i0, i1;
+    int64_t t_first, t_last;
+
+    __device__ __forceinline__ explicit TcWalk(const ChunkShare &s) : at(s.ts), te(s.te), slot(s.slot), first(s.first) {}
+
+    __device__ __forceinline__ bool next(const ChunkArgs &a)
+    {
+        if (at >= te) return false;
+        g = chunk_group<kTcTok, kTcKeys>(a, slot);
+        while (at >= first + 2 * (int64_t)g.nt) {  // empty slots between two groups
+            first += 2 * (int64_t)g.nt;
+            g = chunk_group<kTcTok, kTcKeys>(a, ++slot);
+        }
+        hd = at >= first + g.nt ? 1 : 0;
+        const int64_t item = first + (int64_t)hd * g.nt;
+        i0 = (int)(at - item);
+        i1 = te - item < g.nt ? (int)(te - item) : g.nt;
+        at = item + i1;
+        t_first = g.t0 > 0 ? g.t0 : 0;
+        t_last = g.t0 + g.nq - 1;
+        return true;
+    }
+
+    // does any row of the item see key j
+    __device__ __forceinline__ bool any_sees(const ChunkArgs &a, int64_t j) const
+    {
+        return j <= t_last && (a.window <= 0 || t_first - j < a.window || j < a.sinks);
+    }
+};
+
+// 16 e4m3 codes -> 16 bf16 values times s1 (and s2)
+__device__ __forceinline__ uint32_t bmul2(uint32_t x, uint32_t s)
+{
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&s));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// A code's sign and its 7 low bits, put at the top of a bf16, are its value times 2^-120.  A row's
+// scale 2^(byte - 127) and 2^120 are one bf16 factor up to byte 134, two beyond (byte 255: NaN).
+struct RowScale {
+    uint32_t s1, s2;
+    bool two;
+};
+__device__ __forceinline__ RowScale row_scale(uint32_t byte)
+{
+    RowScale r;
+    const uint32_t b1 = byte == 255u ? 0x7FC0u : ((byte > 134u ? 254u : byte + 120u) << 7);
+    const uint32_t b2 = byte > 134u ? (byte - 7u) << 7 : 0x3F80u;
+    r.s1 = b1 * 0x10001u;
+    r.s2 = b2 * 0x10001u;
+    r.two = byte > 134u;
+    return r;
+}
+
+__device__ __forceinline__ void codes_to_slot(const uint4 &codes, const RowScale &sc, uint32_t row_addr, uint32_t unit,
+                                              uint32_t sw)
+{
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t hi = (w[i] & 0x80808080u) | ((w[i] >> 4) & 0x07070707u), lo = (w[i] << 4) & 0xF0F0F0F0u;
+        o[2 * i] = bmul2(__byte_perm(lo, hi, 0x5140), sc.s1);
+        o[2 * i + 1] = bmul2(__byte_perm(lo, hi, 0x7362), sc.s1);
+    }
+    if (sc.two) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = bmul2(o[i], sc.s2);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                     ::"r"(row_addr + (((unit + h) ^ sw) << 4)), "r"(o[4 * h]), "r"(o[4 * h + 1]), "r"(o[4 * h + 2]),
+                       "r"(o[4 * h + 3])
+                     : "memory");
+}
+
+template <bool kFp8>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcCfg<kFp8>::kThreads, 1)
+chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, int64_t *__restrict__ prefix)
+{
+    using C = TcCfg<kFp8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = smem, *ring = smem + C::kOffRing;
+    TcShared *sh = reinterpret_cast<TcShared *>(smem + C::kOffShared);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cta_rank();
+    const int64_t worker = blockIdx.x >> 1, workers = gridDim.x >> 1;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&sh->kv_full[i], 2 * C::kLoaders);
+            mbar_init(&sh->kv_empty[i], 1);
+        }
+        mbar_init(&sh->q_full, 1);
+        mbar_init(&sh->q_peer, 1);
+        mbar_init(&sh->q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh->s_full[i], 1);
+            mbar_init(&sh->p_full[i], 8);
+        }
+        mbar_init(&sh->pv_done, 1);
+        mbar_init(&sh->o_full, 1);
+        mbar_init(&sh->o_empty, 8);
+        sh->abort_flag = 0;
+        fence_barrier_init();
+    }
+    pdl_enter();  // before the allocation: no CTA waits while it holds tensor memory
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(&sh->tmem_base)), "r"(kTcCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    chunk_share<kTcTok, kTcKeys, C::kThreads>(a, worker, workers, &sh->share, sh->scan,
+                                              blockIdx.x == 0 ? prefix : nullptr);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers are initialised
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem_base;
+    volatile int *abort_flag = &sh->abort_flag;
+    TcWalk it(sh->share);
+    bool ok = true;
+    if (warp == 0) {
+        // ---------------- Q ----------------
+        uint32_t n = 0;
+        while (ok && it.next(a)) {
+            ok = mbar_wait(&sh->q_empty, (n & 1) ^ 1, abort_flag);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            if (lane == 0) mbar_arrive_expect_tx(&sh->q_full, kTcQ);
+            __syncwarp();
+            const int row = (int)rank * 128 + lane * 4, tok = row / kGrp;
+            const int32_t y = tok < it.g.nq ? (int32_t)(it.g.row0 + tok) : (int32_t)a.total_q;  // outside: zeros
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                tma_load_3d(sQ + c * kTcQChunk + lane * 512, &map_q, &sh->q_full, c * 64, it.hd * kGrp + row % kGrp, y);
+            ++n;
+        }
+    } else if (warp == 1) {
+        if (elect_one()) {
+            uint32_t stage = 0, ph = 0, n = 0;
+            auto advance = [&]() {
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    ph ^= 1u;
+                }
+            };
+            if (rank == 0) {
+                // ---------------- products ----------------
+                constexpr uint32_t idesc_s = idesc_bf16_f32(256, kTcKeys, 0, 0);
+                constexpr uint32_t idesc_o = idesc_bf16_f32(256, kD, 0, 1);
+                const uint32_t q_addr = smem_u32(sQ), ring_u = smem_u32(ring);
+                uint32_t T = 0;  // tiles so far
+                auto slot_full = [&]() -> bool { return wait_pair(&sh->kv_full[stage], ph, abort_flag); };
+                auto do_s = [&](uint32_t t) -> bool {
+                    if (!slot_full()) return false;
+                    tc_fence_after();
+                    const uint32_t k_addr = ring_u + stage * kTcSlot, d = tmem + (t & 1) * kTcKeys;
+#pragma unroll
+                    for (int ks = 0; ks < kD / 16; ++ks)
+                        mma2_ss(d, sdesc_sw128(q_addr + (ks >> 2) * kTcQChunk + (ks & 3) * 32, 16, 1024),
+                                sdesc_sw128(k_addr + (ks >> 2) * kTcKChunk + (ks & 3) * 32, 16, 1024), idesc_s,
+                                ks > 0 ? 1u : 0u);
+                    commit_both(&sh->kv_empty[stage]);
+                    commit_both(&sh->s_full[t & 1]);
+                    advance();
+                    return true;
+                };
+                while (ok && it.next(a)) {
+                    const int nt = it.i1 - it.i0;
+                    ok = wait_pair(&sh->q_full, n & 1, abort_flag) && wait_pair(&sh->q_peer, n & 1, abort_flag);
+                    ok = ok && do_s(T);
+                    if (ok && nt == 1) commit_both(&sh->q_empty);
+                    for (int i = 0; ok && i < nt; ++i, ++T) {
+                        if (i + 1 < nt) {
+                            if (!(ok = do_s(T + 1))) break;
+                            if (i + 2 == nt) commit_both(&sh->q_empty);
+                        }
+                        if (i == 0 && !(ok = wait_pair(&sh->o_empty, (n & 1) ^ 1, abort_flag))) break;
+                        if (!(ok = wait_pair(&sh->p_full[T & 1], (T >> 1) & 1, abort_flag))) break;
+                        if (!(ok = slot_full())) break;
+                        tc_fence_after();
+                        const uint32_t v_addr = ring_u + stage * kTcSlot, p = tmem + (T & 1) * kTcKeys;
+#pragma unroll
+                        for (int ks = 0; ks < kTcKeys / 16; ++ks)
+                            mma2_ts(tmem + kTcO, p + ks * 8, sdesc_sw128(v_addr + ks * 2048, kTcVChunk, 1024), idesc_o,
+                                    (i == 0 && ks == 0) ? 0u : 1u);
+                        commit_both(&sh->kv_empty[stage]);
+                        commit_both(&sh->pv_done);
+                        if (i + 1 == nt) commit_both(&sh->o_full);
+                        advance();
+                    }
+                    ++n;
+                }
+            } else {
+                // ---------------- CTA 1: its Q is there ----------------
+                while (ok && it.next(a)) {
+                    ok = mbar_wait(&sh->q_full, n & 1, abort_flag);
+                    if (ok) arrive_leader(&sh->q_peer);
+                    ++n;
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp < 4) {
+        if (!kFp8) {
+            // ---------------- bf16 K and V ----------------
+            // A lane's pool rows (row of the KV head, -1: none) are those of keys lane + 32 e.  Two
+            // half tiles are on their way while the next is issued.
+            const int w = warp - 2, u = lane & 7, k4 = lane >> 3;
+            const uint32_t ring_u = smem_u32(ring);
+            const uint8_t *kp = static_cast<const uint8_t *>(a.pool.k) + u * 16;
+            const uint8_t *vp = static_cast<const uint8_t *>(a.pool.v) + u * 16 + rank * 256;
+            uint32_t stage = 0, ph = 1, issued = 0, done = 0, done_stage = 0;
+            auto complete = [&]() {  // the oldest half tile on its way has arrived
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_leader(&sh->kv_full[done_stage]);
+                if (++done_stage == C::kStages) done_stage = 0;
+                ++done;
+            };
+            auto slot_ready = [&]() -> bool {
+                const bool good = mbar_wait(&sh->kv_empty[stage], ph, abort_flag);
+                return __all_sync(0xffffffffu, good);
+            };
+            auto slot_issued = [&]() {
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    ph ^= 1u;
+                }
+                if (++issued - done > 2) {
+                    asm volatile("cp.async.wait_group 2;" ::: "memory");
+                    complete();
+                }
+            };
+            while (ok && it.next(a)) {
+                auto key_rows = [&](int i, int32_t (&r)[4]) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int64_t j = tile_start(it.g, i, kTcKeys) + lane + 32 * e;
+                        r[e] = -1;
+                        if (i < it.i1 && it.any_sees(a, j)) {
+                            const int64_t row = chunk_pool_row(a.pool, it.g.s, j);
+                            if (row >= 0) r[e] = (int32_t)(row * kHKV + it.hd);
+                        }
+                    }
+                };
+                auto load_k = [&](const int32_t (&r)[4]) -> bool {  // this warp: keys 32 w .. of the CTA's 64
+                    if (!slot_ready()) return false;
+                    const int32_t mine = rank == 0 ? (w == 0 ? r[0] : r[1]) : (w == 0 ? r[2] : r[3]);
+                    const uint32_t dst = ring_u + stage * kTcSlot + (w * 32 + k4) * 128;
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        const int32_t row = __shfl_sync(0xffffffffu, mine, x * 4 + k4);
+                        const uint8_t *src = kp + (int64_t)(row < 0 ? 0 : row) * 512;
+                        const uint32_t d = dst + x * 512 + (((uint32_t)u ^ ((x * 4 + k4) & 7)) << 4);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) copy16(d + c * kTcKChunk, src + c * 128, row >= 0);
+                    }
+                    slot_issued();
+                    return true;
+                };
+                auto load_v = [&](const int32_t (&r)[4]) -> bool {  // this warp: keys 64 w .. of the 128
+                    if (!slot_ready()) return false;
+                    const uint32_t dst = ring_u + stage * kTcSlot + (w * 64 + k4) * 128;
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const int32_t lo = x < 8 ? r[0] : r[1], hi = x < 8 ? r[2] : r[3];
+                        const int32_t row = __shfl_sync(0xffffffffu, w == 0 ? lo : hi, (x * 4 + k4) & 31);
+                        const uint8_t *src = vp + (int64_t)(row < 0 ? 0 : row) * 512;
+                        const uint32_t d = dst + x * 512 + (((uint32_t)u ^ ((x * 4 + k4) & 7)) << 4);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) copy16(d + c * kTcVChunk, src + c * 128, row >= 0);
+                    }
+                    slot_issued();
+                    return true;
+                };
+                int32_t r0[4], r1[4], r2[4];
+                key_rows(it.i0, r0);
+                key_rows(it.i0 + 1, r1);
+                ok = load_k(r0);
+                for (int i = it.i0; ok && i < it.i1; ++i) {
+                    key_rows(i + 2, r2);
+                    if (i + 1 < it.i1) ok = load_k(r1);
+                    ok = ok && load_v(r0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        r0[e] = r1[e];
+                        r1[e] = r2[e];
+                    }
+                }
+            }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            while (ok && done != issued) complete();
+        }
+    } else if (warp < 8) {
+        // ---------------- softmax and epilogue ----------------
+        const int quad = warp & 3, r = (int)rank * 128 + quad * 32 + lane;
+        const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+        const float c2 = a.scale * 1.4426950408889634f;
+        uint32_t T = 0, n = 0;
+        while (ok && it.next(a)) {
+            const int64_t t = it.g.t0 + r / kGrp;  // this row's position (rows past the tokens: not written)
+            float m = -INFINITY, l = 0.f;          // running maximum of c2 s, sum of exp2(c2 s - m)
+            for (int i = it.i0; i < it.i1; ++i, ++T) {
+                const uint32_t buf = T & 1;
+                ok = mbar_wait(&sh->s_full[buf], (T >> 1) & 1, abort_flag);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                float s[kTcKeys];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(lane_addr + buf * kTcKeys + c * 32, s + c * 32);
+                tmem_wait_ld();
+                const int64_t j0 = tile_start(it.g, i, kTcKeys);
+                // unless every row sees every key of the tile: columns hi and below, from lo on or below sk
+                if (!(it.g.t0 >= 0 && j0 + kTcKeys - 1 <= it.g.t0 &&
+                      (a.window <= 0 || it.t_last - j0 < a.window || j0 + kTcKeys <= a.sinks))) {
+                    const int64_t d = t - j0, w = a.window > 0 ? d - a.window + 1 : 0, k = a.sinks - j0;
+                    const int hi = (int)(d < -1 ? -1 : (d > kTcKeys ? kTcKeys : d));
+                    const int lo = (int)(w < 0 ? 0 : (w > kTcKeys ? kTcKeys : w));
+                    const int sk = (int)(k < 0 ? 0 : (k > kTcKeys ? kTcKeys : k));
+#pragma unroll
+                    for (int c = 0; c < kTcKeys; ++c)
+                        if (c > hi || (c < lo && c >= sk)) s[c] = -INFINITY;
+                }
+                float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
+#pragma unroll
+                for (int c = 4; c < kTcKeys; c += 4) {
+                    x0 = fmaxf(x0, s[c]);
+                    x1 = fmaxf(x1, s[c + 1]);
+                    x2 = fmaxf(x2, s[c + 2]);
+                    x3 = fmaxf(x3, s[c + 3]);
+                }
+                const float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * c2;
+                // move the maximum: O and l are zero until a key is visible, rescaled after that
+                const bool grow = m != -INFINITY && mx > m + kTcRescale;
+                if (__any_sync(0xffffffffu, grow)) {
+                    const float f = grow ? ex2(m - mx) : 1.f;
+                    if (grow) m = mx;
+                    l *= f;
+                    // O of the tiles before: T - 1 products have completed at least (S(T) came behind them)
+                    ok = mbar_wait(&sh->pv_done, (T - 1) & 1, abort_flag);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < kD / 32; ++c) {
+                        float o[32];
+                        tmem_ld32(lane_addr + kTcO + c * 32, o);
+                        tmem_wait_ld();
+                        uint32_t w[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
+                        tmem_st32u(lane_addr + kTcO + c * 32, w);
+                    }
+                }
+                if (m == -INFINITY) m = mx;
+                const float base = m == -INFINITY ? 0.f : m;
+                float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const int c = h * 64 + 2 * e;
+                        const float p0 = ex2(fmaf(s[c], c2, -base)), p1 = ex2(fmaf(s[c + 1], c2, -base));
+                        const float p2 = ex2(fmaf(s[c + 2], c2, -base)), p3 = ex2(fmaf(s[c + 3], c2, -base));
+                        l0 += p0;
+                        l1 += p1;
+                        l2 += p2;
+                        l3 += p3;
+                        const __nv_bfloat162 a0 = __floats2bfloat162_rn(p0, p1), a1 = __floats2bfloat162_rn(p2, p3);
+                        p[e] = *reinterpret_cast<const uint32_t *>(&a0);
+                        p[e + 1] = *reinterpret_cast<const uint32_t *>(&a1);
+                    }
+                    tmem_st32u(lane_addr + buf * kTcKeys + h * 32, p);
+                }
+                l += (l0 + l1) + (l2 + l3);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_leader(&sh->p_full[buf]);
+            }
+            if (!ok) break;
+            // O of the whole item
+            ok = mbar_wait(&sh->o_full, n & 1, abort_flag);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
+            tc_fence_after();
+            const bool mine = r / kGrp < it.g.nq && r < kTcRows, none = l == 0.f;
+            const float inv = none ? 0.f : 1.f / l;
+            const bool complete = it.i0 == 0 && it.i1 == it.g.nt;
+            const int64_t piece = 2 * worker + (it.i0 == 0 ? 1 : 0);
+            const int64_t row = (it.g.row0 + r / kGrp) * kHQ + it.hd * kGrp + r % kGrp;
+            const float lse2 = none ? -INFINITY : m + log2f(l);
+#pragma unroll 1
+            for (int c = 0; c < kD / 32; ++c) {
+                float o[32];
+                tmem_ld32(lane_addr + kTcO + c * 32, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
+                if (!mine) continue;
+                if (complete) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        __nv_bfloat162 h[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) h[x] = __floats2bfloat162_rn(o[e + 2 * x], o[e + 2 * x + 1]);
+                        *reinterpret_cast<uint4 *>(a.o + row * kD + c * 32 + e) = *reinterpret_cast<const uint4 *>(h);
+                    }
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(a.ws + (piece * kTcRows + r) * kD + c * 32);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_leader(&sh->o_empty);
+            if (mine && complete && a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
+            ++n;
+            if (mine && !complete) a.ws[2 * workers * kTcRows * kD + piece * kTcRows + r] = lse2;
+        }
+    } else if (kFp8) {
+        // ---------------- e4m3 codes to bf16 ----------------
+        TcTable *tab = reinterpret_cast<TcTable *>(smem + C::kOffTable);
+        const int ct = threadIdx.x - 256, cw = ct >> 5, k8 = lane >> 2, piece = lane & 3;
+        const uint32_t ring_u = smem_u32(ring);
+        const uint8_t *kp = static_cast<const uint8_t *>(a.pool.k), *vp = static_cast<const uint8_t *>(a.pool.v);
+        uint32_t stage = 0, ph = 1;
+        while (it.next(a)) {  // to the end also after a wait that gave up: the four warps meet at barriers
+            const int nt = it.i1 - it.i0;
+            // the pool row of key ct of the item's tile i, -1: none
+            auto key_row = [&](int i) -> int32_t {
+                if (i >= nt) return -1;
+                const int64_t j = tile_start(it.g, it.i0 + i, kTcKeys) + ct;
+                if (!it.any_sees(a, j)) return -1;
+                const uint32_t p = (uint32_t)j / (uint32_t)a.pool.page_size, off = (uint32_t)j - p * (uint32_t)a.pool.page_size;
+                const int32_t page = p < (uint32_t)a.pool.max_pages ? __ldg(a.pool.table + (int64_t)it.g.s * a.pool.max_pages + p) : -1;
+                if (page < 0 || page >= a.pool.num_pages) {
+                    set_device_status(QSA_ERR_DEVICE_CHECK);
+                    return -1;
+                }
+                return (int32_t)((int64_t)page * a.pool.page_size + off);
+            };
+            auto scale_byte = [&](const uint8_t *sc, int32_t row) -> uint32_t {
+                return row >= 0 ? __ldg(sc + (int64_t)row * kHKV + it.hd) : 127u;
+            };
+            auto put = [&](int i, int32_t row, uint32_t kb, uint32_t vb) {
+                tab->row[i % 3][ct] = row;
+                tab->ks[i % 3][ct] = (uint8_t)kb;
+                tab->vs[i % 3][ct] = (uint8_t)vb;
+            };
+            uint4 kreg[8], vreg[8];
+            uint32_t kb[2], vb[4];
+            auto load_k = [&](int i) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int key = (int)rank * 64 + cw * 16 + q * 8 + k8;
+                    const int32_t row = tab->row[i % 3][key];
+                    kb[q] = tab->ks[i % 3][key];
+                    const uint8_t *src = kp + ((int64_t)row * kHKV + it.hd) * kD + piece * 16;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        kreg[q * 4 + c] = row >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            auto load_v = [&](int i) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int key = cw * 32 + q * 8 + k8;
+                    const int32_t row = tab->row[i % 3][key];
+                    vb[q] = tab->vs[i % 3][key];
+                    const uint8_t *src = vp + ((int64_t)row * kHKV + it.hd) * kD + rank * 128 + piece * 16;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        vreg[q * 2 + c] = row >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            auto slot_ready = [&]() -> bool {
+                ok = ok && mbar_wait(&sh->kv_empty[stage], ph, abort_flag);
+                return ok = __all_sync(0xffffffffu, ok);
+            };
+            auto slot_done = [&]() {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive_leader(&sh->kv_full[stage]);
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    ph ^= 1u;
+                }
+            };
+            // the tables run ahead: tile i + 1's is written while tile i is converted, its rows and
+            // scales were fetched one step earlier, the pages of the tile after it two steps
+            int32_t row_b = key_row(0), row_a;
+            put(0, row_b, scale_byte(a.pool.k_scales, row_b), scale_byte(a.pool.v_scales, row_b));
+            row_b = key_row(1);
+            uint32_t nkb = scale_byte(a.pool.k_scales, row_b), nvb = scale_byte(a.pool.v_scales, row_b);
+            row_a = key_row(2);
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            load_k(0);
+            for (int i = 0; i <= nt; ++i) {
+                put(i + 1, row_b, nkb, nvb);
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                row_b = row_a;
+                nkb = scale_byte(a.pool.k_scales, row_b);
+                nvb = scale_byte(a.pool.v_scales, row_b);
+                row_a = key_row(i + 3);
+                if (i < nt && slot_ready()) {  // K(i)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const RowScale sc = row_scale(kb[q]);
+                        const uint32_t dst = ring_u + stage * kTcSlot + (cw * 16 + q * 8 + k8) * 128;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) codes_to_slot(kreg[q * 4 + c], sc, dst + c * kTcKChunk, 2 * piece, k8);
+                    }
+                    slot_done();
+                }
+                if (i + 1 < nt) load_k(i + 1);
+                if (i > 0 && slot_ready()) {  // V(i - 1)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const RowScale sc = row_scale(vb[q]);
+                        const uint32_t dst = ring_u + stage * kTcSlot + (cw * 32 + q * 8 + k8) * 128;
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) codes_to_slot(vreg[q * 2 + c], sc, dst + c * kTcVChunk, 2 * piece, k8);
+                    }
+                    slot_done();
+                }
+                if (i < nt) load_v(i);
+            }
+            // the next item's tables overwrite this one's
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // no arrival of the peer is under way
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcCols) : "memory");
+    }
+}
+
+// pairs of CTAs that run at the same time on the current device
+template <bool kFp8>
+cudaError_t tc_workers(int64_t *out)
+{
+    static std::mutex mu;
+    static int known[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 64 && known[dev] > 0) {
+        *out = known[dev];
+        return cudaSuccess;
+    }
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * kTcMaxPairs);
+    cfg.blockDim = dim3(TcCfg<kFp8>::kThreads);
+    cfg.dynamicSmemBytes = TcCfg<kFp8>::kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, chunk_tc_kernel<kFp8>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    if (n > kTcMaxPairs) n = (int)kTcMaxPairs;
+    if (dev < 64) known[dev] = n;
+    *out = n;
+    return cudaSuccess;
+}
+
+size_t tc_prefix_offset() { return (size_t)(2 * kTcMaxPairs) * kTcRows * (kD + 1) * sizeof(float); }
+
+template <bool kFp8>
+cudaError_t launch_tc(const ChunkArgs &a, cudaStream_t stream)
+{
+    CUtensorMap mq;
+    if (!make_tmap_3d(&mq, a.q, kD, kHQ, (uint64_t)a.total_q, kD * 2, (uint64_t)kHQ * kD * 2, 64, 4, 1))
+        return cudaErrorInvalidValue;
+    cudaError_t e = set_smem_attr_once(reinterpret_cast<const void *>(chunk_tc_kernel<kFp8>), TcCfg<kFp8>::kSmem);
+    if (e != cudaSuccess) return e;
+    int64_t workers = 0;
+    e = tc_workers<kFp8>(&workers);
+    if (e != cudaSuccess) return e;
+    int64_t *prefix = reinterpret_cast<int64_t *>(reinterpret_cast<uint8_t *>(a.ws) + tc_prefix_offset());
+    e = launch_pdl(chunk_tc_kernel<kFp8>, dim3((unsigned)(2 * workers)), dim3(TcCfg<kFp8>::kThreads), TcCfg<kFp8>::kSmem,
+                   stream, mq, a, prefix);
+    if (e != cudaSuccess) return e;
+    return launch_chunk_merge<kTcTok, kTcKeys>(a, prefix, workers, stream);
+}
+
+}  // namespace
+
+size_t chunk_tc_workspace_bytes(int batch, int64_t total_q)
+{
+    return tc_prefix_offset() + (size_t)(chunk_slots<kTcTok>(total_q, batch) + 1) * sizeof(int64_t);
+}
+
+cudaError_t launch_chunk_tc(const ChunkArgs &a, cudaStream_t stream)
+{
+    return a.pool.fp8 ? launch_tc<true>(a, stream) : launch_tc<false>(a, stream);
+}
+
+}  // namespace qsa

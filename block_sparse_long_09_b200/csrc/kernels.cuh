@@ -331,6 +331,9 @@ struct ChunkArgs {
 };
 size_t chunk_workspace_bytes(int batch, int64_t total_q);
 cudaError_t launch_chunk_attn(const ChunkArgs &a, cudaStream_t stream);
+// its kernel for several new tokens per sequence (attn_chunk_tc.cu)
+size_t chunk_tc_workspace_bytes(int batch, int64_t total_q);
+cudaError_t launch_chunk_tc(const ChunkArgs &a, cudaStream_t stream);
 
 // tensor-map creation (host), defined in api.cu
 bool make_tmap_2d(CUtensorMap *map, const void *base, uint64_t inner, uint64_t outer,
