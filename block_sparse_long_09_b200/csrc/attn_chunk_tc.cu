@@ -18,9 +18,10 @@
 //   warps 2, 3   (bf16 pools) K and V half tiles into a ring of five 32 KB slots, by 16-byte
 //                asynchronous copies: pages of any size, and zeros for keys that no row of the
 //                item sees.  (TMA gathers of four rows by index took 75 cycles per 512 bytes.)
-//   warps 4..7   softmax, a thread per row; running maxima move (and O is rescaled) only when a
-//                row's maximum grows by more than 2^8
-//   warps 8..11  (e4m3 pools) codes to bf16 in registers, exactly: the 7 low bits moved to the
+//   warps 4..11  softmax, two threads per row (64 keys each, two warps per scheduler: one alone took
+//                2700 cycles per tile); running maxima move, and O is rescaled, only when a row's
+//                maximum grows by more than 2^8, so that the two rarely have to exchange them
+//   warps 12..15 (e4m3 pools) codes to bf16 in registers, exactly: the 7 low bits moved to the
 //                top of a bf16, times 2^120 times the row's scale; then to one of four slots
 // Work is shared out and cut items are merged as chunk_common.cuh describes.  Every wait is bounded.
 #include <mutex>
@@ -46,7 +47,8 @@ struct TcShared {
     uint64_t pv_done, o_full, o_empty;
     uint32_t tmem_base;
     int abort_flag;
-    int64_t scan[12];
+    int64_t scan[16];
+    float half[2][128];  // row maxima, and at an item's end row sums, of the two halves of the keys
     ChunkShare share;
 };
 
@@ -57,7 +59,7 @@ struct TcTable {  // e4m3: pool rows and scale bytes of a tile's keys (a ring of
 
 template <bool kFp8>
 struct TcCfg {
-    static constexpr int kThreads = kFp8 ? 384 : 256;
+    static constexpr int kThreads = kFp8 ? 512 : 384;
     static constexpr int kStages = kFp8 ? 4 : 5;
     static constexpr int kLoaders = kFp8 ? 4 : 2;  // warps of a CTA that fill the slots
     static constexpr int kOffRing = kTcQ;
@@ -178,13 +180,26 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// barrier of the 256 softmax threads that also ORs a predicate over them
+__device__ __forceinline__ bool softmax_any(bool x)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, 2, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r) : "r"((uint32_t)x) : "memory");
+    return r != 0;
+}
+
 // The items of a share, in order: every role walks the same list.
 struct TcWalk {
     int64_t at, te, slot, first;
     // the current item
     ChunkGroup g;
     int hd, i0, i1;
-    int64_t t_first, t_last;
+    int t_first, t_last;  // positions of the first (at least 0) and the last token
 
     __device__ __forceinline__ explicit TcWalk(const ChunkShare &s) : at(s.ts), te(s.te), slot(s.slot), first(s.first) {}
 
@@ -201,15 +216,38 @@ struct TcWalk {
         i0 = (int)(at - item);
         i1 = te - item < g.nt ? (int)(te - item) : g.nt;
         at = item + i1;
-        t_first = g.t0 > 0 ? g.t0 : 0;
-        t_last = g.t0 + g.nq - 1;
+        t_first = g.t0 > 0 ? (int)g.t0 : 0;
+        t_last = (int)(g.t0 + g.nq - 1);
         return true;
     }
 
     // does any row of the item see key j
-    __device__ __forceinline__ bool any_sees(const ChunkArgs &a, int64_t j) const
+    __device__ __forceinline__ bool any_sees(const ChunkArgs &a, int j) const
     {
         return j <= t_last && (a.window <= 0 || t_first - j < a.window || j < a.sinks);
+    }
+
+    // A key's place in the pool, in two steps, so that the page's load is not waited for: its page
+    // (kUnseen: no row of the item sees the key, kNoPage: not in the table) and its row there.
+    static constexpr int32_t kUnseen = -2, kNoPage = -1;
+    __device__ __forceinline__ int32_t page_of(const ChunkArgs &a, int i, int key, uint32_t *off) const
+    {
+        if (i >= i1) return kUnseen;
+        const int j = (int)tile_start(g, i, kTcKeys) + key;
+        if (!any_sees(a, j)) return kUnseen;
+        const uint32_t ps = (uint32_t)a.pool.page_size, p = (uint32_t)j / ps;
+        *off = (uint32_t)j - p * ps;
+        return p < (uint32_t)a.pool.max_pages ? __ldg(a.pool.table + (int64_t)g.s * a.pool.max_pages + p) : kNoPage;
+    }
+    // the row of this KV head, -1: none
+    __device__ __forceinline__ int32_t row_of(const ChunkArgs &a, int32_t page, uint32_t off) const
+    {
+        if (page == kUnseen) return -1;
+        if (page < 0 || page >= a.pool.num_pages) {
+            set_device_status(QSA_ERR_DEVICE_CHECK);
+            return -1;
+        }
+        return (int32_t)(((int64_t)page * a.pool.page_size + off) * kHKV + hd);
     }
 };
 
@@ -282,11 +320,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
         mbar_init(&sh->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->s_full[i], 1);
-            mbar_init(&sh->p_full[i], 8);
+            mbar_init(&sh->p_full[i], 16);
         }
         mbar_init(&sh->pv_done, 1);
         mbar_init(&sh->o_full, 1);
-        mbar_init(&sh->o_empty, 8);
+        mbar_init(&sh->o_empty, 16);
         sh->abort_flag = 0;
         fence_barrier_init();
     }
@@ -420,16 +458,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                 }
             };
             while (ok && it.next(a)) {
-                auto key_rows = [&](int i, int32_t (&r)[4]) {
+                int32_t page[4];
+                uint32_t off[4] = {0u, 0u, 0u, 0u};
+                auto fetch = [&](int i) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int64_t j = tile_start(it.g, i, kTcKeys) + lane + 32 * e;
-                        r[e] = -1;
-                        if (i < it.i1 && it.any_sees(a, j)) {
-                            const int64_t row = chunk_pool_row(a.pool, it.g.s, j);
-                            if (row >= 0) r[e] = (int32_t)(row * kHKV + it.hd);
-                        }
-                    }
+                    for (int e = 0; e < 4; ++e) page[e] = it.page_of(a, i, lane + 32 * e, &off[e]);
+                };
+                auto resolve = [&](int32_t (&r)[4]) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) r[e] = it.row_of(a, page[e], off[e]);
                 };
                 auto load_k = [&](const int32_t (&r)[4]) -> bool {  // this warp: keys 32 w .. of the CTA's 64
                     if (!slot_ready()) return false;
@@ -461,124 +498,129 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                     slot_issued();
                     return true;
                 };
-                int32_t r0[4], r1[4], r2[4];
-                key_rows(it.i0, r0);
-                key_rows(it.i0 + 1, r1);
+                int32_t r0[4], r1[4];
+                fetch(it.i0);
+                resolve(r0);
+                fetch(it.i0 + 1);
                 ok = load_k(r0);
                 for (int i = it.i0; ok && i < it.i1; ++i) {
-                    key_rows(i + 2, r2);
+                    resolve(r1);
+                    fetch(i + 2);
                     if (i + 1 < it.i1) ok = load_k(r1);
                     ok = ok && load_v(r0);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        r0[e] = r1[e];
-                        r1[e] = r2[e];
-                    }
+                    for (int e = 0; e < 4; ++e) r0[e] = r1[e];
                 }
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             while (ok && done != issued) complete();
         }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         // ---------------- softmax and epilogue ----------------
-        const int quad = warp & 3, r = (int)rank * 128 + quad * 32 + lane;
+        // Two threads per row: half of a tile's keys, half of O's dims.  After a wait that gave up they
+        // go on to the end without waiting: the eight warps meet at barriers.
+        constexpr int kHalf = kTcKeys / 2;
+        const int quad = warp & 3, half = (warp - 4) >> 2, rl = quad * 32 + lane, r = (int)rank * 128 + rl;
         const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
         const float c2 = a.scale * 1.4426950408889634f;
         uint32_t T = 0, n = 0;
-        while (ok && it.next(a)) {
+        auto await = [&](uint64_t *bar, uint32_t parity) {
+            ok = ok && mbar_wait(bar, parity, abort_flag);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+        };
+        while (it.next(a)) {
             const int64_t t = it.g.t0 + r / kGrp;  // this row's position (rows past the tokens: not written)
-            float m = -INFINITY, l = 0.f;          // running maximum of c2 s, sum of exp2(c2 s - m)
+            float m = -INFINITY, l = 0.f;          // running maximum of c2 s, sum of this half's exp2(c2 s - m)
             for (int i = it.i0; i < it.i1; ++i, ++T) {
                 const uint32_t buf = T & 1;
-                ok = mbar_wait(&sh->s_full[buf], (T >> 1) & 1, abort_flag);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                tc_fence_after();
-                float s[kTcKeys];
+                await(&sh->s_full[buf], (T >> 1) & 1);
+                float s[kHalf];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(lane_addr + buf * kTcKeys + c * 32, s + c * 32);
+                for (int c = 0; c < 2; ++c) tmem_ld32(lane_addr + buf * kTcKeys + half * kHalf + c * 32, s + c * 32);
                 tmem_wait_ld();
                 const int64_t j0 = tile_start(it.g, i, kTcKeys);
                 // unless every row sees every key of the tile: columns hi and below, from lo on or below sk
                 if (!(it.g.t0 >= 0 && j0 + kTcKeys - 1 <= it.g.t0 &&
                       (a.window <= 0 || it.t_last - j0 < a.window || j0 + kTcKeys <= a.sinks))) {
-                    const int64_t d = t - j0, w = a.window > 0 ? d - a.window + 1 : 0, k = a.sinks - j0;
-                    const int hi = (int)(d < -1 ? -1 : (d > kTcKeys ? kTcKeys : d));
-                    const int lo = (int)(w < 0 ? 0 : (w > kTcKeys ? kTcKeys : w));
-                    const int sk = (int)(k < 0 ? 0 : (k > kTcKeys ? kTcKeys : k));
+                    const int64_t j1 = j0 + half * kHalf, d = t - j1, w = a.window > 0 ? d - a.window + 1 : 0, k = a.sinks - j1;
+                    const int hi = (int)(d < -1 ? -1 : (d > kHalf ? kHalf : d));
+                    const int lo = (int)(w < 0 ? 0 : (w > kHalf ? kHalf : w));
+                    const int sk = (int)(k < 0 ? 0 : (k > kHalf ? kHalf : k));
 #pragma unroll
-                    for (int c = 0; c < kTcKeys; ++c)
+                    for (int c = 0; c < kHalf; ++c)
                         if (c > hi || (c < lo && c >= sk)) s[c] = -INFINITY;
                 }
                 float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
 #pragma unroll
-                for (int c = 4; c < kTcKeys; c += 4) {
+                for (int c = 4; c < kHalf; c += 4) {
                     x0 = fmaxf(x0, s[c]);
                     x1 = fmaxf(x1, s[c + 1]);
                     x2 = fmaxf(x2, s[c + 2]);
                     x3 = fmaxf(x3, s[c + 3]);
                 }
-                const float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * c2;
-                // move the maximum: O and l are zero until a key is visible, rescaled after that
-                const bool grow = m != -INFINITY && mx > m + kTcRescale;
-                if (__any_sync(0xffffffffu, grow)) {
+                float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * c2;
+                // Also the point from which the halves' P may overwrite S: both have been read.
+                if (softmax_any(m == -INFINITY ? mx > m : mx > m + kTcRescale)) {
+                    sh->half[half][rl] = mx;
+                    asm volatile("bar.sync 2, 256;" ::: "memory");
+                    mx = fmaxf(mx, sh->half[half ^ 1][rl]);
+                    // O and l are zero until a key is visible, rescaled after that
+                    const bool grow = m != -INFINITY && mx > m + kTcRescale;
                     const float f = grow ? ex2(m - mx) : 1.f;
-                    if (grow) m = mx;
-                    l *= f;
-                    // O of the tiles before: T - 1 products have completed at least (S(T) came behind them)
-                    ok = mbar_wait(&sh->pv_done, (T - 1) & 1, abort_flag);
-                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    tc_fence_after();
+                    if (grow || m == -INFINITY) m = mx;
+                    if (__any_sync(0xffffffffu, grow)) {
+                        l *= f;
+                        // O of the tiles before: T - 1 products have completed at least (S(T) came behind them)
+                        await(&sh->pv_done, (T - 1) & 1);
 #pragma unroll 1
-                    for (int c = 0; c < kD / 32; ++c) {
-                        float o[32];
-                        tmem_ld32(lane_addr + kTcO + c * 32, o);
-                        tmem_wait_ld();
-                        uint32_t w[32];
+                        for (int c = 0; c < 4; ++c) {
+                            float o[32];
+                            tmem_ld32(lane_addr + kTcO + half * 128 + c * 32, o);
+                            tmem_wait_ld();
+                            uint32_t w[32];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
-                        tmem_st32u(lane_addr + kTcO + c * 32, w);
+                            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
+                            tmem_st32u(lane_addr + kTcO + half * 128 + c * 32, w);
+                        }
                     }
                 }
-                if (m == -INFINITY) m = mx;
                 const float base = m == -INFINITY ? 0.f : m;
                 float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+                uint32_t p[32];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const int c = h * 64 + 2 * e;
-                        const float p0 = ex2(fmaf(s[c], c2, -base)), p1 = ex2(fmaf(s[c + 1], c2, -base));
-                        const float p2 = ex2(fmaf(s[c + 2], c2, -base)), p3 = ex2(fmaf(s[c + 3], c2, -base));
-                        l0 += p0;
-                        l1 += p1;
-                        l2 += p2;
-                        l3 += p3;
-                        const __nv_bfloat162 a0 = __floats2bfloat162_rn(p0, p1), a1 = __floats2bfloat162_rn(p2, p3);
-                        p[e] = *reinterpret_cast<const uint32_t *>(&a0);
-                        p[e + 1] = *reinterpret_cast<const uint32_t *>(&a1);
-                    }
-                    tmem_st32u(lane_addr + buf * kTcKeys + h * 32, p);
+                for (int e = 0; e < 32; e += 2) {
+                    const float p0 = ex2(fmaf(s[2 * e], c2, -base)), p1 = ex2(fmaf(s[2 * e + 1], c2, -base));
+                    const float p2 = ex2(fmaf(s[2 * e + 2], c2, -base)), p3 = ex2(fmaf(s[2 * e + 3], c2, -base));
+                    l0 += p0;
+                    l1 += p1;
+                    l2 += p2;
+                    l3 += p3;
+                    const __nv_bfloat162 a0 = __floats2bfloat162_rn(p0, p1), a1 = __floats2bfloat162_rn(p2, p3);
+                    p[e] = *reinterpret_cast<const uint32_t *>(&a0);
+                    p[e + 1] = *reinterpret_cast<const uint32_t *>(&a1);
                 }
+                tmem_st32u(lane_addr + buf * kTcKeys + half * 32, p);
                 l += (l0 + l1) + (l2 + l3);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_leader(&sh->p_full[buf]);
             }
-            if (!ok) break;
+            asm volatile("bar.sync 2, 256;" ::: "memory");  // the maxima have been read
+            sh->half[half][rl] = l;
+            asm volatile("bar.sync 2, 256;" ::: "memory");
+            l += sh->half[half ^ 1][rl];
             // O of the whole item
-            ok = mbar_wait(&sh->o_full, n & 1, abort_flag);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            tc_fence_after();
-            const bool mine = r / kGrp < it.g.nq && r < kTcRows, none = l == 0.f;
+            await(&sh->o_full, n & 1);
+            ++n;
+            const bool mine = ok && r / kGrp < it.g.nq && r < kTcRows, none = l == 0.f;
             const float inv = none ? 0.f : 1.f / l;
             const bool complete = it.i0 == 0 && it.i1 == it.g.nt;
             const int64_t piece = 2 * worker + (it.i0 == 0 ? 1 : 0);
             const int64_t row = (it.g.row0 + r / kGrp) * kHQ + it.hd * kGrp + r % kGrp;
-            const float lse2 = none ? -INFINITY : m + log2f(l);
 #pragma unroll 1
-            for (int c = 0; c < kD / 32; ++c) {
+            for (int c = half * 4; c < half * 4 + 4; ++c) {
                 float o[32];
                 tmem_ld32(lane_addr + kTcO + c * 32, o);
                 tmem_wait_ld();
@@ -602,34 +644,23 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_leader(&sh->o_empty);
-            if (mine && complete && a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
-            ++n;
-            if (mine && !complete) a.ws[2 * workers * kTcRows * kD + piece * kTcRows + r] = lse2;
+            if (mine && half == 0) {
+                const float lse2 = none ? -INFINITY : m + log2f(l);
+                if (!complete) a.ws[2 * workers * kTcRows * kD + piece * kTcRows + r] = lse2;
+                else if (a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
+            }
         }
     } else if (kFp8) {
         // ---------------- e4m3 codes to bf16 ----------------
         TcTable *tab = reinterpret_cast<TcTable *>(smem + C::kOffTable);
-        const int ct = threadIdx.x - 256, cw = ct >> 5, k8 = lane >> 2, piece = lane & 3;
+        const int ct = threadIdx.x - 384, cw = ct >> 5, k8 = lane >> 2, piece = lane & 3;
         const uint32_t ring_u = smem_u32(ring);
         const uint8_t *kp = static_cast<const uint8_t *>(a.pool.k), *vp = static_cast<const uint8_t *>(a.pool.v);
         uint32_t stage = 0, ph = 1;
         while (it.next(a)) {  // to the end also after a wait that gave up: the four warps meet at barriers
             const int nt = it.i1 - it.i0;
-            // the pool row of key ct of the item's tile i, -1: none
-            auto key_row = [&](int i) -> int32_t {
-                if (i >= nt) return -1;
-                const int64_t j = tile_start(it.g, it.i0 + i, kTcKeys) + ct;
-                if (!it.any_sees(a, j)) return -1;
-                const uint32_t p = (uint32_t)j / (uint32_t)a.pool.page_size, off = (uint32_t)j - p * (uint32_t)a.pool.page_size;
-                const int32_t page = p < (uint32_t)a.pool.max_pages ? __ldg(a.pool.table + (int64_t)it.g.s * a.pool.max_pages + p) : -1;
-                if (page < 0 || page >= a.pool.num_pages) {
-                    set_device_status(QSA_ERR_DEVICE_CHECK);
-                    return -1;
-                }
-                return (int32_t)((int64_t)page * a.pool.page_size + off);
-            };
             auto scale_byte = [&](const uint8_t *sc, int32_t row) -> uint32_t {
-                return row >= 0 ? __ldg(sc + (int64_t)row * kHKV + it.hd) : 127u;
+                return row >= 0 ? __ldg(sc + row) : 127u;
             };
             auto put = [&](int i, int32_t row, uint32_t kb, uint32_t vb) {
                 tab->row[i % 3][ct] = row;
@@ -644,7 +675,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                     const int key = (int)rank * 64 + cw * 16 + q * 8 + k8;
                     const int32_t row = tab->row[i % 3][key];
                     kb[q] = tab->ks[i % 3][key];
-                    const uint8_t *src = kp + ((int64_t)row * kHKV + it.hd) * kD + piece * 16;
+                    const uint8_t *src = kp + (int64_t)row * kD + piece * 16;
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
                         kreg[q * 4 + c] = row >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
@@ -656,7 +687,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                     const int key = cw * 32 + q * 8 + k8;
                     const int32_t row = tab->row[i % 3][key];
                     vb[q] = tab->vs[i % 3][key];
-                    const uint8_t *src = vp + ((int64_t)row * kHKV + it.hd) * kD + rank * 128 + piece * 16;
+                    const uint8_t *src = vp + (int64_t)row * kD + rank * 128 + piece * 16;
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
                         vreg[q * 2 + c] = row >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
@@ -675,22 +706,24 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                     ph ^= 1u;
                 }
             };
-            // the tables run ahead: tile i + 1's is written while tile i is converted, its rows and
-            // scales were fetched one step earlier, the pages of the tile after it two steps
-            int32_t row_b = key_row(0), row_a;
+            // the tables run ahead: tile i + 1's is written while tile i is converted, its scales were
+            // fetched one step earlier, its pages two
+            uint32_t off = 0u;
+            int32_t page = it.page_of(a, it.i0, ct, &off), row_b = it.row_of(a, page, off);
             put(0, row_b, scale_byte(a.pool.k_scales, row_b), scale_byte(a.pool.v_scales, row_b));
-            row_b = key_row(1);
+            page = it.page_of(a, it.i0 + 1, ct, &off);
+            row_b = it.row_of(a, page, off);
             uint32_t nkb = scale_byte(a.pool.k_scales, row_b), nvb = scale_byte(a.pool.v_scales, row_b);
-            row_a = key_row(2);
+            page = it.page_of(a, it.i0 + 2, ct, &off);
             asm volatile("bar.sync 1, 128;" ::: "memory");
             load_k(0);
             for (int i = 0; i <= nt; ++i) {
                 put(i + 1, row_b, nkb, nvb);
                 asm volatile("bar.sync 1, 128;" ::: "memory");
-                row_b = row_a;
+                row_b = it.row_of(a, page, off);
                 nkb = scale_byte(a.pool.k_scales, row_b);
                 nvb = scale_byte(a.pool.v_scales, row_b);
-                row_a = key_row(i + 3);
+                page = it.page_of(a, it.i0 + i + 3, ct, &off);
                 if (i < nt && slot_ready()) {  // K(i)
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
