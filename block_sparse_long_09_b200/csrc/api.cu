@@ -200,9 +200,16 @@ qsa::CachePool pool_of(int32_t format, const void *k_pages, const void *v_pages,
                        const uint8_t *v_scales, int64_t num_pages, int32_t page_size, const int32_t *block_table,
                        int32_t max_pages)
 {
+    // Division of 31-bit numbers by d, 2^(b-1) < d <= 2^b: m = floor(2^(31+b) / d) + 1 (or the quotient
+    // itself for a power of two) exceeds 2^(31+b) / d by at most one, so x m / 2^(31+b) exceeds
+    // x / d by at most x / 2^(31+b) < 2^-b <= 1 / d: the floor is the same.
+    uint32_t b = 0;
+    while (((int64_t)1 << b) < page_size) ++b;
+    const uint64_t top = (uint64_t)1 << (31 + b);
+    const uint32_t mul = (uint32_t)(top / (uint64_t)page_size + (top % (uint64_t)page_size != 0 ? 1 : 0));
     return qsa::CachePool{const_cast<void *>(k_pages), const_cast<void *>(v_pages), const_cast<uint8_t *>(k_scales),
                           const_cast<uint8_t *>(v_scales), format == QSA_CACHE_E4M3 ? 1 : 0, num_pages, page_size,
-                          block_table, max_pages};
+                          block_table, max_pages, mul, 31 + b};
 }
 
 }  // namespace

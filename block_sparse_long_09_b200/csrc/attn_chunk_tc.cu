@@ -14,7 +14,9 @@
 // tile i is done, whose 128 exponentials per row (1024 cycles of an SM's exp2 units)
 // take half of the 2048 cycles of the tile's two products.
 //   warp 0       Q, once per item (TMA)
-//   warp 1       CTA 0: issues the products of both CTAs; CTA 1: passes on to CTA 0 that its Q is there
+//   warp 1       CTA 0: issues the products of both CTAs; CTA 1: passes on to CTA 0 that its Q and
+//                slots are full.  The fence between the slots' writers and the tensor cores stands
+//                here: in a writer it would wait for the copies that are still on their way
 //   warps 2, 3   (bf16 pools) K and V half tiles into a ring of five 32 KB slots, by 16-byte
 //                asynchronous copies: pages of any size, and zeros for keys that no row of the
 //                item sees.  (TMA gathers of four rows by index took 75 cycles per 512 bytes.)
@@ -41,7 +43,7 @@ constexpr float kTcRescale = 8.f;
 constexpr int64_t kTcMaxPairs = 80;
 
 struct TcShared {
-    uint64_t kv_full[kTcMaxStages], kv_empty[kTcMaxStages];
+    uint64_t kv_full[kTcMaxStages], kv_peer[kTcMaxStages], kv_empty[kTcMaxStages];
     uint64_t q_full, q_peer, q_empty;
     uint64_t s_full[2], p_full[2];
     uint64_t pv_done, o_full, o_empty;
@@ -61,7 +63,7 @@ template <bool kFp8>
 struct TcCfg {
     static constexpr int kThreads = kFp8 ? 512 : 384;
     static constexpr int kStages = kFp8 ? 4 : 5;
-    static constexpr int kLoaders = kFp8 ? 4 : 2;  // warps of a CTA that fill the slots
+    static constexpr int kFills = kFp8 ? 4 : 64;  // arrivals that fill a slot: warps that convert, threads that copy
     static constexpr int kOffRing = kTcQ;
     static constexpr int kOffTable = kOffRing + kStages * kTcSlot;
     static constexpr int kOffShared = kOffTable + (kFp8 ? (int)sizeof(TcTable) : 0);
@@ -200,6 +202,8 @@ struct TcWalk {
     ChunkGroup g;
     int hd, i0, i1;
     int t_first, t_last;  // positions of the first (at least 0) and the last token
+    int near, sinks;      // some row sees the keys near .. t_last and those below sinks
+    const int32_t *table; // the sequence's row of the block table
 
     __device__ __forceinline__ explicit TcWalk(const ChunkShare &s) : at(s.ts), te(s.te), slot(s.slot), first(s.first) {}
 
@@ -218,13 +222,16 @@ struct TcWalk {
         at = item + i1;
         t_first = g.t0 > 0 ? (int)g.t0 : 0;
         t_last = (int)(g.t0 + g.nq - 1);
+        near = a.window > 0 ? t_first - (int)a.window + 1 : 0;
+        sinks = (int)a.sinks;
+        table = a.pool.table + (int64_t)g.s * a.pool.max_pages;
         return true;
     }
 
     // does any row of the item see key j
-    __device__ __forceinline__ bool any_sees(const ChunkArgs &a, int j) const
+    __device__ __forceinline__ bool any_sees(int j) const
     {
-        return j <= t_last && (a.window <= 0 || t_first - j < a.window || j < a.sinks);
+        return j <= t_last && (j >= near || j < sinks);
     }
 
     // A key's place in the pool, in two steps, so that the page's load is not waited for: its page
@@ -233,21 +240,20 @@ struct TcWalk {
     __device__ __forceinline__ int32_t page_of(const ChunkArgs &a, int i, int key, uint32_t *off) const
     {
         if (i >= i1) return kUnseen;
-        const int j = (int)tile_start(g, i, kTcKeys) + key;
-        if (!any_sees(a, j)) return kUnseen;
-        const uint32_t ps = (uint32_t)a.pool.page_size, p = (uint32_t)j / ps;
-        *off = (uint32_t)j - p * ps;
-        return p < (uint32_t)a.pool.max_pages ? __ldg(a.pool.table + (int64_t)g.s * a.pool.max_pages + p) : kNoPage;
+        const int j = (i < g.ns ? i : (int)g.w_tile + (i - g.ns)) * kTcKeys + key;
+        if (!any_sees(j)) return kUnseen;
+        const uint32_t p = a.pool.page_of((uint32_t)j, off);
+        return p < (uint32_t)a.pool.max_pages ? __ldg(table + p) : kNoPage;
     }
     // the row of this KV head, -1: none
     __device__ __forceinline__ int32_t row_of(const ChunkArgs &a, int32_t page, uint32_t off) const
     {
         if (page == kUnseen) return -1;
-        if (page < 0 || page >= a.pool.num_pages) {
+        if ((uint32_t)page >= (uint32_t)a.pool.num_pages) {
             set_device_status(QSA_ERR_DEVICE_CHECK);
             return -1;
         }
-        return (int32_t)(((int64_t)page * a.pool.page_size + off) * kHKV + hd);
+        return ((int32_t)page * a.pool.page_size + (int32_t)off) * kHKV + hd;  // (a pool has fewer than 2^31 rows)
     }
 };
 
@@ -312,7 +318,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
     const int64_t worker = blockIdx.x >> 1, workers = gridDim.x >> 1;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
-            mbar_init(&sh->kv_full[i], 2 * C::kLoaders);
+            mbar_init(&sh->kv_full[i], C::kFills);
+            mbar_init(&sh->kv_peer[i], 1);
             mbar_init(&sh->kv_empty[i], 1);
         }
         mbar_init(&sh->q_full, 1);
@@ -374,7 +381,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                 constexpr uint32_t idesc_o = idesc_bf16_f32(256, kD, 0, 1);
                 const uint32_t q_addr = smem_u32(sQ), ring_u = smem_u32(ring);
                 uint32_t T = 0;  // tiles so far
-                auto slot_full = [&]() -> bool { return wait_pair(&sh->kv_full[stage], ph, abort_flag); };
+                auto slot_full = [&]() -> bool {
+                    if (!mbar_wait(&sh->kv_full[stage], ph, abort_flag)) return false;
+                    fence_proxy_async_smem();
+                    return wait_pair(&sh->kv_peer[stage], ph, abort_flag);
+                };
                 auto do_s = [&](uint32_t t) -> bool {
                     if (!slot_full()) return false;
                     tc_fence_after();
@@ -416,10 +427,18 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                     ++n;
                 }
             } else {
-                // ---------------- CTA 1: its Q is there ----------------
+                // ---------------- CTA 1: its Q and slots are full ----------------
                 while (ok && it.next(a)) {
-                    ok = mbar_wait(&sh->q_full, n & 1, abort_flag);
-                    if (ok) arrive_leader(&sh->q_peer);
+                    for (int e = 0; ok && e < 2 * (it.i1 - it.i0); ++e) {
+                        ok = mbar_wait(&sh->kv_full[stage], ph, abort_flag);
+                        fence_proxy_async_smem();
+                        if (ok) arrive_leader(&sh->kv_peer[stage]);
+                        advance();
+                        if (e == 0 && ok) {
+                            ok = mbar_wait(&sh->q_full, n & 1, abort_flag);
+                            if (ok) arrive_leader(&sh->q_peer);
+                        }
+                    }
                     ++n;
                 }
             }
@@ -428,53 +447,43 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
     } else if (warp < 4) {
         if (!kFp8) {
             // ---------------- bf16 K and V ----------------
-            // A lane's pool rows (row of the KV head, -1: none) are those of keys lane + 32 e.  Two
-            // half tiles are on their way while the next is issued.
+            // Warp w copies K of the keys 32 w .. of the CTA's 64, and V of these and of the same keys of
+            // the other CTA's 64; a lane looks up one key of each (row of the KV head, -1: none).  A slot's
+            // barrier counts the threads whose copies have arrived.
             const int w = warp - 2, u = lane & 7, k4 = lane >> 3;
             const uint32_t ring_u = smem_u32(ring);
             const uint8_t *kp = static_cast<const uint8_t *>(a.pool.k) + u * 16;
             const uint8_t *vp = static_cast<const uint8_t *>(a.pool.v) + u * 16 + rank * 256;
-            uint32_t stage = 0, ph = 1, issued = 0, done = 0, done_stage = 0;
-            auto complete = [&]() {  // the oldest half tile on its way has arrived
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive_leader(&sh->kv_full[done_stage]);
-                if (++done_stage == C::kStages) done_stage = 0;
-                ++done;
-            };
+            uint32_t stage = 0, ph = 1;
             auto slot_ready = [&]() -> bool {
                 const bool good = mbar_wait(&sh->kv_empty[stage], ph, abort_flag);
                 return __all_sync(0xffffffffu, good);
             };
             auto slot_issued = [&]() {
-                asm volatile("cp.async.commit_group;" ::: "memory");
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];"
+                             ::"r"(smem_u32(&sh->kv_full[stage])) : "memory");
                 if (++stage == C::kStages) {
                     stage = 0;
                     ph ^= 1u;
                 }
-                if (++issued - done > 2) {
-                    asm volatile("cp.async.wait_group 2;" ::: "memory");
-                    complete();
-                }
             };
             while (ok && it.next(a)) {
-                int32_t page[4];
-                uint32_t off[4] = {0u, 0u, 0u, 0u};
+                int32_t page[2];
+                uint32_t off[2] = {0u, 0u};
                 auto fetch = [&](int i) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) page[e] = it.page_of(a, i, lane + 32 * e, &off[e]);
+                    for (int e = 0; e < 2; ++e) page[e] = it.page_of(a, i, ((int)rank ^ e) * 64 + w * 32 + lane, &off[e]);
                 };
-                auto resolve = [&](int32_t (&r)[4]) {
+                auto resolve = [&](int32_t (&r)[2]) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) r[e] = it.row_of(a, page[e], off[e]);
+                    for (int e = 0; e < 2; ++e) r[e] = it.row_of(a, page[e], off[e]);
                 };
-                auto load_k = [&](const int32_t (&r)[4]) -> bool {  // this warp: keys 32 w .. of the CTA's 64
+                auto load_k = [&](const int32_t (&r)[2]) -> bool {
                     if (!slot_ready()) return false;
-                    const int32_t mine = rank == 0 ? (w == 0 ? r[0] : r[1]) : (w == 0 ? r[2] : r[3]);
                     const uint32_t dst = ring_u + stage * kTcSlot + (w * 32 + k4) * 128;
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
-                        const int32_t row = __shfl_sync(0xffffffffu, mine, x * 4 + k4);
+                        const int32_t row = __shfl_sync(0xffffffffu, r[0], x * 4 + k4);
                         const uint8_t *src = kp + (int64_t)(row < 0 ? 0 : row) * 512;
                         const uint32_t d = dst + x * 512 + (((uint32_t)u ^ ((x * 4 + k4) & 7)) << 4);
 #pragma unroll
@@ -483,22 +492,22 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                     slot_issued();
                     return true;
                 };
-                auto load_v = [&](const int32_t (&r)[4]) -> bool {  // this warp: keys 64 w .. of the 128
+                auto load_v = [&](const int32_t (&r)[2]) -> bool {
                     if (!slot_ready()) return false;
-                    const uint32_t dst = ring_u + stage * kTcSlot + (w * 64 + k4) * 128;
 #pragma unroll
                     for (int x = 0; x < 16; ++x) {
-                        const int32_t lo = x < 8 ? r[0] : r[1], hi = x < 8 ? r[2] : r[3];
-                        const int32_t row = __shfl_sync(0xffffffffu, w == 0 ? lo : hi, (x * 4 + k4) & 31);
+                        const int key = (x & 7) * 4 + k4;
+                        const uint32_t dst = ring_u + stage * kTcSlot + (((int)rank ^ (x >> 3)) * 64 + w * 32 + key) * 128;
+                        const int32_t row = __shfl_sync(0xffffffffu, r[x >> 3], key);
                         const uint8_t *src = vp + (int64_t)(row < 0 ? 0 : row) * 512;
-                        const uint32_t d = dst + x * 512 + (((uint32_t)u ^ ((x * 4 + k4) & 7)) << 4);
+                        const uint32_t d = dst + (((uint32_t)u ^ (key & 7)) << 4);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) copy16(d + c * kTcVChunk, src + c * 128, row >= 0);
                     }
                     slot_issued();
                     return true;
                 };
-                int32_t r0[4], r1[4];
+                int32_t r0[2], r1[2];
                 fetch(it.i0);
                 resolve(r0);
                 fetch(it.i0 + 1);
@@ -509,11 +518,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                     if (i + 1 < it.i1) ok = load_k(r1);
                     ok = ok && load_v(r0);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) r0[e] = r1[e];
+                    for (int e = 0; e < 2; ++e) r0[e] = r1[e];
                 }
             }
-            asm volatile("cp.async.wait_group 0;" ::: "memory");
-            while (ok && done != issued) complete();
+            asm volatile("cp.async.wait_all;" ::: "memory");  // none is on its way when the CTA exits
         }
     } else if (warp < 12) {
         // ---------------- softmax and epilogue ----------------
@@ -698,9 +706,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                 return ok = __all_sync(0xffffffffu, ok);
             };
             auto slot_done = [&]() {
-                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) arrive_leader(&sh->kv_full[stage]);
+                if (lane == 0) mbar_arrive(&sh->kv_full[stage]);
                 if (++stage == C::kStages) {
                     stage = 0;
                     ph ^= 1u;

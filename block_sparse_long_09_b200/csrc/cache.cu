@@ -30,10 +30,11 @@ constexpr int kRowVals = 512;  // values of one token: 2 KV heads x 256
 __device__ __forceinline__ int64_t pool_row(const CachePool &c, int64_t s, int64_t tok)
 {
     if (tok < 0) return -1;
-    const int64_t j = tok / c.page_size;
-    const int32_t page = j < c.max_pages ? __ldg(c.table + s * c.max_pages + j) : -1;
+    uint32_t off;
+    const uint32_t j = c.page_of((uint32_t)tok, &off);  // (a length is an int32)
+    const int32_t page = j < (uint32_t)c.max_pages ? __ldg(c.table + s * c.max_pages + j) : -1;
     if (page < 0 || page >= c.num_pages) return -1;
-    return (int64_t)page * c.page_size + tok % c.page_size;
+    return (int64_t)page * c.page_size + off;
 }
 
 __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }

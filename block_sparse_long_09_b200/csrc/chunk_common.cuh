@@ -154,13 +154,14 @@ __device__ __forceinline__ bool chunk_sees(int64_t t, int64_t j, int64_t window,
 // the pool row of position j of sequence s, -1 (flagged) when the table has no valid page
 __device__ __forceinline__ int64_t chunk_pool_row(const CachePool &c, int64_t s, int64_t j)
 {
-    const int64_t p = j / c.page_size;
-    const int32_t page = p < c.max_pages ? __ldg(c.table + s * c.max_pages + p) : -1;
+    uint32_t off;
+    const uint32_t p = c.page_of((uint32_t)j, &off);
+    const int32_t page = p < (uint32_t)c.max_pages ? __ldg(c.table + s * c.max_pages + p) : -1;
     if (page < 0 || page >= c.num_pages) {
         set_device_status(QSA_ERR_DEVICE_CHECK);
         return -1;
     }
-    return (int64_t)page * c.page_size + j % c.page_size;
+    return (int64_t)page * c.page_size + off;
 }
 
 constexpr int kMergeWarps = 8, kMergeThreads = kMergeWarps * 32;

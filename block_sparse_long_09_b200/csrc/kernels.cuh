@@ -295,6 +295,15 @@ struct CachePool {
     int page_size;
     const int32_t *table;           // [batch, max_pages]
     int max_pages;
+    uint32_t div_mul, div_shift;    // x / page_size = (x * div_mul) >> div_shift for x < 2^31
+
+    // page and row in it of position x < 2^31
+    __device__ __forceinline__ uint32_t page_of(uint32_t x, uint32_t *off) const
+    {
+        const uint32_t p = (uint32_t)(((uint64_t)x * div_mul) >> div_shift);
+        *off = x - p * (uint32_t)page_size;
+        return p;
+    }
 };
 
 // the scale 2^(byte - 127) of an e4m3 row; 255 stands for a row with a non-finite value
