@@ -93,6 +93,17 @@ __device__ __forceinline__ void arrive_leader(uint64_t *bar)
         ::"r"(smem_u32(bar)) : "memory");
 }
 
+// the same without a release: for what tcgen05 fences order (a release at the cluster's scope waits for
+// the thread's global stores)
+__device__ __forceinline__ void arrive_leader_relaxed(uint64_t *bar)
+{
+    asm volatile(
+        "{\n\t.reg .b32 r;\n\t"
+        "mapa.shared::cluster.u32 r, %0, 0;\n\t"
+        "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [r];\n\t}"
+        ::"r"(smem_u32(bar)) : "memory");
+}
+
 __device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity)
 {
     uint32_t ok;
@@ -613,7 +624,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_leader(&sh->p_full[buf]);
+                if (lane == 0) arrive_leader_relaxed(&sh->p_full[buf]);
             }
             asm volatile("bar.sync 2, 256;" ::: "memory");  // the maxima have been read
             sh->half[half][rl] = l;
@@ -651,7 +662,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_leader(&sh->o_empty);
+            if (lane == 0) arrive_leader_relaxed(&sh->o_empty);
             if (mine && half == 0) {
                 const float lse2 = none ? -INFINITY : m + log2f(l);
                 if (!complete) a.ws[2 * workers * kTcRows * kD + piece * kTcRows + r] = lse2;
