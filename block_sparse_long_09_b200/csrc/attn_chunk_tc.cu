@@ -17,13 +17,13 @@
 //   warp 1       CTA 0: issues the products of both CTAs; CTA 1: passes on to CTA 0 that its Q and
 //                slots are full.  The fence between the slots' writers and the tensor cores stands
 //                here: in a writer it would wait for the copies that are still on their way
-//   warps 2, 3   (bf16 pools) K and V half tiles into a ring of five 32 KB slots, by 16-byte
+//   warps 2, 3   bf16 pools: K and V half tiles into a ring of five 32 KB slots, by 16-byte
 //                asynchronous copies: pages of any size, and zeros for keys that no row of the
 //                item sees.  (TMA gathers of four rows by index took 75 cycles per 512 bytes.)
-//   warps 4..11  softmax, two threads per row (64 keys each, two warps per scheduler: one alone took
-//                2700 cycles per tile); running maxima move, and O is rescaled, only when a row's
-//                maximum grows by more than 2^8, so that the two rarely have to exchange them
-//   warps 12..15 (e4m3 pools) codes to bf16 in registers, exactly: the 7 low bits moved to the
+//                e4m3 pools: the pool rows and scales of the tiles' keys, into a ring of tables
+//   warps 4..7   softmax, a thread per row; running maxima move (and O is rescaled) only when a
+//                row's maximum grows by more than 2^8
+//   warps 8..15  (e4m3 pools) codes to bf16 in registers, exactly: the 7 low bits moved to the
 //                top of a bf16, times 2^120 times the row's scale; then to one of four slots
 // Work is shared out and cut items are merged as chunk_common.cuh describes.  Every wait is bounded.
 #include <mutex>
@@ -35,7 +35,7 @@ namespace qsa {
 namespace {
 
 constexpr int kTcTok = 21, kTcRows = kTcTok * kGrp, kTcKeys = 128;
-constexpr int kTcSlot = 32768, kTcMaxStages = 5;
+constexpr int kTcSlot = 32768, kTcMaxStages = 5, kTcTables = 4;
 constexpr int kTcQ = 128 * kD * 2;
 constexpr int kTcQChunk = 128 * 128, kTcKChunk = 64 * 128, kTcVChunk = 128 * 128;
 constexpr uint32_t kTcO = 256, kTcCols = 512;
@@ -47,23 +47,23 @@ struct TcShared {
     uint64_t q_full, q_peer, q_empty;
     uint64_t s_full[2], p_full[2];
     uint64_t pv_done, o_full, o_empty;
+    uint64_t tab_full[kTcTables], tab_empty[kTcTables];
     uint32_t tmem_base;
     int abort_flag;
     int64_t scan[16];
-    float half[2][128];  // row maxima, and at an item's end row sums, of the two halves of the keys
     ChunkShare share;
 };
 
-struct TcTable {  // e4m3: pool rows and scale bytes of a tile's keys (a ring of three tiles)
-    int32_t row[3][kTcKeys];
-    uint8_t ks[3][kTcKeys], vs[3][kTcKeys];
+struct TcTable {  // e4m3: pool rows (of the KV head, -1: none) and scale bytes of a tile's keys
+    int32_t row[kTcTables][kTcKeys];
+    uint8_t ks[kTcTables][kTcKeys], vs[kTcTables][kTcKeys];
 };
 
 template <bool kFp8>
 struct TcCfg {
-    static constexpr int kThreads = kFp8 ? 512 : 384;
+    static constexpr int kThreads = kFp8 ? 512 : 256;
     static constexpr int kStages = kFp8 ? 4 : 5;
-    static constexpr int kFills = kFp8 ? 4 : 64;  // arrivals that fill a slot: warps that convert, threads that copy
+    static constexpr int kFills = kFp8 ? 8 : 64;  // arrivals that fill a slot: warps that convert, threads that copy
     static constexpr int kOffRing = kTcQ;
     static constexpr int kOffTable = kOffRing + kStages * kTcSlot;
     static constexpr int kOffShared = kOffTable + (kFp8 ? (int)sizeof(TcTable) : 0);
@@ -184,6 +184,18 @@ __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t *v)
         : "memory");
 }
 
+// 16 columns times f
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float *v, float f)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+        " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "f"(v[0] * f), "f"(v[1] * f), "f"(v[2] * f), "f"(v[3] * f), "f"(v[4] * f), "f"(v[5] * f),
+          "f"(v[6] * f), "f"(v[7] * f), "f"(v[8] * f), "f"(v[9] * f), "f"(v[10] * f), "f"(v[11] * f),
+          "f"(v[12] * f), "f"(v[13] * f), "f"(v[14] * f), "f"(v[15] * f)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x)
@@ -191,19 +203,6 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-// barrier of the 256 softmax threads that also ORs a predicate over them
-__device__ __forceinline__ bool softmax_any(bool x)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, 2, 256, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r) : "r"((uint32_t)x) : "memory");
-    return r != 0;
 }
 
 // The items of a share, in order: every role walks the same list.
@@ -338,11 +337,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
         mbar_init(&sh->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->s_full[i], 1);
-            mbar_init(&sh->p_full[i], 16);
+            mbar_init(&sh->p_full[i], 8);
         }
         mbar_init(&sh->pv_done, 1);
         mbar_init(&sh->o_full, 1);
-        mbar_init(&sh->o_empty, 16);
+        mbar_init(&sh->o_empty, 8);
+        for (int i = 0; i < kTcTables; ++i) {
+            mbar_init(&sh->tab_full[i], 2);
+            mbar_init(&sh->tab_empty[i], 8);
+        }
         sh->abort_flag = 0;
         fence_barrier_init();
     }
@@ -533,113 +536,159 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");  // none is on its way when the CTA exits
+        } else {
+            // ---------------- rows and scales of e4m3 pools ----------------
+            // Two keys per lane; a tile's pages are looked up one tile ahead of its scales, and these
+            // one ahead of the table's writing.
+            TcTable *tab = reinterpret_cast<TcTable *>(smem + C::kOffTable);
+            const int key = (warp - 2) * 64 + lane;
+            uint32_t n = 0;  // tables written
+            while (ok && it.next(a)) {
+                int32_t page[2], row[2];
+                uint32_t off[2] = {0u, 0u}, kb[2], vb[2];
+                auto fetch = [&](int i) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) page[e] = it.page_of(a, i, key + 32 * e, &off[e]);
+                };
+                auto resolve = [&]() {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        row[e] = it.row_of(a, page[e], off[e]);
+                        kb[e] = row[e] >= 0 ? __ldg(a.pool.k_scales + row[e]) : 127u;
+                        vb[e] = row[e] >= 0 ? __ldg(a.pool.v_scales + row[e]) : 127u;
+                    }
+                };
+                fetch(it.i0);
+                resolve();
+                fetch(it.i0 + 1);
+                for (int i = it.i0; i < it.i1; ++i, ++n) {
+                    const int32_t r0 = row[0], r1 = row[1];
+                    const uint32_t k0 = kb[0], k1 = kb[1], v0 = vb[0], v1 = vb[1], x = n % kTcTables;
+                    resolve();
+                    fetch(i + 2);
+                    ok = mbar_wait(&sh->tab_empty[x], ((n / kTcTables) & 1) ^ 1, abort_flag);
+                    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                    tab->row[x][key] = r0;
+                    tab->row[x][key + 32] = r1;
+                    tab->ks[x][key] = (uint8_t)k0;
+                    tab->ks[x][key + 32] = (uint8_t)k1;
+                    tab->vs[x][key] = (uint8_t)v0;
+                    tab->vs[x][key + 32] = (uint8_t)v1;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->tab_full[x]);
+                }
+            }
         }
-    } else if (warp < 12) {
+    } else if (warp < 8) {
         // ---------------- softmax and epilogue ----------------
-        // Two threads per row: half of a tile's keys, half of O's dims.  After a wait that gave up they
-        // go on to the end without waiting: the eight warps meet at barriers.
         constexpr int kHalf = kTcKeys / 2;
-        const int quad = warp & 3, half = (warp - 4) >> 2, rl = quad * 32 + lane, r = (int)rank * 128 + rl;
+        const int quad = warp & 3, rl = quad * 32 + lane, r = (int)rank * 128 + rl;
         const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
         const float c2 = a.scale * 1.4426950408889634f;
         uint32_t T = 0, n = 0;
-        auto await = [&](uint64_t *bar, uint32_t parity) {
-            ok = ok && mbar_wait(bar, parity, abort_flag);
+        auto await = [&](uint64_t *bar, uint32_t parity) -> bool {
+            ok = mbar_wait(bar, parity, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
+            return ok;
         };
-        while (it.next(a)) {
+        while (ok && it.next(a)) {
             const int64_t t = it.g.t0 + r / kGrp;  // this row's position (rows past the tokens: not written)
-            float m = -INFINITY, l = 0.f;          // running maximum of c2 s, sum of this half's exp2(c2 s - m)
+            float m = -INFINITY, l = 0.f;          // running maximum of c2 s, sum of exp2(c2 s - m)
             for (int i = it.i0; i < it.i1; ++i, ++T) {
-                const uint32_t buf = T & 1;
-                await(&sh->s_full[buf], (T >> 1) & 1);
-                float s[kHalf];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) tmem_ld32(lane_addr + buf * kTcKeys + half * kHalf + c * 32, s + c * 32);
-                tmem_wait_ld();
+                const uint32_t buf = T & 1, s_addr = lane_addr + buf * kTcKeys;
+                if (!await(&sh->s_full[buf], (T >> 1) & 1)) break;
                 const int64_t j0 = tile_start(it.g, i, kTcKeys);
                 // unless every row sees every key of the tile: columns hi and below, from lo on or below sk
-                if (!(it.g.t0 >= 0 && j0 + kTcKeys - 1 <= it.g.t0 &&
-                      (a.window <= 0 || it.t_last - j0 < a.window || j0 + kTcKeys <= a.sinks))) {
-                    const int64_t j1 = j0 + half * kHalf, d = t - j1, w = a.window > 0 ? d - a.window + 1 : 0, k = a.sinks - j1;
-                    const int hi = (int)(d < -1 ? -1 : (d > kHalf ? kHalf : d));
-                    const int lo = (int)(w < 0 ? 0 : (w > kHalf ? kHalf : w));
-                    const int sk = (int)(k < 0 ? 0 : (k > kHalf ? kHalf : k));
+                const bool edge = !(it.g.t0 >= 0 && j0 + kTcKeys - 1 <= it.g.t0 &&
+                                    (a.window <= 0 || it.t_last - j0 < a.window || j0 + kTcKeys <= a.sinks));
+                const int64_t d64 = t - j0, w64 = a.window > 0 ? d64 - a.window + 1 : 0, k64 = a.sinks - j0;
+                const int hi = (int)(d64 < -1 ? -1 : (d64 > kTcKeys ? kTcKeys : d64));
+                const int lo = (int)(w64 < 0 ? 0 : (w64 > kTcKeys ? kTcKeys : w64));
+                const int sk = (int)(k64 < 0 ? 0 : (k64 > kTcKeys ? kTcKeys : k64));
+                auto load = [&](int h, float (&s)[kHalf]) {
 #pragma unroll
-                    for (int c = 0; c < kHalf; ++c)
-                        if (c > hi || (c < lo && c >= sk)) s[c] = -INFINITY;
-                }
-                float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
+                    for (int c = 0; c < 2; ++c) tmem_ld32(s_addr + h * kHalf + c * 32, s + c * 32);
+                    tmem_wait_ld();
+                    if (edge) {
 #pragma unroll
-                for (int c = 4; c < kHalf; c += 4) {
-                    x0 = fmaxf(x0, s[c]);
-                    x1 = fmaxf(x1, s[c + 1]);
-                    x2 = fmaxf(x2, s[c + 2]);
-                    x3 = fmaxf(x3, s[c + 3]);
-                }
-                float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * c2;
-                // Also the point from which the halves' P may overwrite S: both have been read.
-                if (softmax_any(m == -INFINITY ? mx > m : mx > m + kTcRescale)) {
-                    sh->half[half][rl] = mx;
-                    asm volatile("bar.sync 2, 256;" ::: "memory");
-                    mx = fmaxf(mx, sh->half[half ^ 1][rl]);
-                    // O and l are zero until a key is visible, rescaled after that
-                    const bool grow = m != -INFINITY && mx > m + kTcRescale;
+                        for (int c = 0; c < kHalf; ++c)
+                            if (h * kHalf + c > hi || (h * kHalf + c < lo && h * kHalf + c >= sk)) s[c] = -INFINITY;
+                    }
+                };
+                auto largest = [&](const float (&s)[kHalf]) -> float {
+                    float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
+#pragma unroll
+                    for (int c = 4; c < kHalf; c += 4) {
+                        x0 = fmaxf(x0, s[c]);
+                        x1 = fmaxf(x1, s[c + 1]);
+                        x2 = fmaxf(x2, s[c + 2]);
+                        x3 = fmaxf(x3, s[c + 3]);
+                    }
+                    return fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+                };
+                // The second half first, for its maximum: bf16 pools keep it in registers; with 16 warps
+                // there is no room for it, and it is read again below.
+                float s0[kHalf], s1[kHalf];
+                load(1, s1);
+                float mx = largest(s1);
+                load(0, s0);
+                mx = fmaxf(mx, largest(s0)) * c2;
+                // O and l are zero until a key is visible, rescaled after that
+                const bool grow = m != -INFINITY && mx > m + kTcRescale;
+                if (__any_sync(0xffffffffu, grow)) {
                     const float f = grow ? ex2(m - mx) : 1.f;
-                    if (grow || m == -INFINITY) m = mx;
-                    if (__any_sync(0xffffffffu, grow)) {
-                        l *= f;
-                        // O of the tiles before: T - 1 products have completed at least (S(T) came behind them)
-                        await(&sh->pv_done, (T - 1) & 1);
+                    if (grow) m = mx;
+                    l *= f;
+                    // O of the tiles before: T - 1 products have completed at least (S(T) came behind them)
+                    if (!await(&sh->pv_done, (T - 1) & 1)) break;
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            float o[32];
-                            tmem_ld32(lane_addr + kTcO + half * 128 + c * 32, o);
-                            tmem_wait_ld();
-                            uint32_t w[32];
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e] * f);
-                            tmem_st32u(lane_addr + kTcO + half * 128 + c * 32, w);
-                        }
+                    for (int c = 0; c < kD / 16; ++c) {
+                        float o[16];
+                        tmem_ld16(lane_addr + kTcO + c * 16, o);
+                        tmem_wait_ld();
+                        tmem_st16(lane_addr + kTcO + c * 16, o, f);
                     }
                 }
+                if (m == -INFINITY) m = mx;
                 const float base = m == -INFINITY ? 0.f : m;
                 float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
-                uint32_t p[32];
+                // keys 64 h .. as columns 32 h ..: the scores there have been read by now
+                auto probabilities = [&](int h, const float (&s)[kHalf]) {
+                    uint32_t p[32];
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const float p0 = ex2(fmaf(s[2 * e], c2, -base)), p1 = ex2(fmaf(s[2 * e + 1], c2, -base));
-                    const float p2 = ex2(fmaf(s[2 * e + 2], c2, -base)), p3 = ex2(fmaf(s[2 * e + 3], c2, -base));
-                    l0 += p0;
-                    l1 += p1;
-                    l2 += p2;
-                    l3 += p3;
-                    const __nv_bfloat162 a0 = __floats2bfloat162_rn(p0, p1), a1 = __floats2bfloat162_rn(p2, p3);
-                    p[e] = *reinterpret_cast<const uint32_t *>(&a0);
-                    p[e + 1] = *reinterpret_cast<const uint32_t *>(&a1);
-                }
-                tmem_st32u(lane_addr + buf * kTcKeys + half * 32, p);
+                    for (int e = 0; e < 32; e += 2) {
+                        const float p0 = ex2(fmaf(s[2 * e], c2, -base)), p1 = ex2(fmaf(s[2 * e + 1], c2, -base));
+                        const float p2 = ex2(fmaf(s[2 * e + 2], c2, -base)), p3 = ex2(fmaf(s[2 * e + 3], c2, -base));
+                        l0 += p0;
+                        l1 += p1;
+                        l2 += p2;
+                        l3 += p3;
+                        const __nv_bfloat162 a0 = __floats2bfloat162_rn(p0, p1), a1 = __floats2bfloat162_rn(p2, p3);
+                        p[e] = *reinterpret_cast<const uint32_t *>(&a0);
+                        p[e + 1] = *reinterpret_cast<const uint32_t *>(&a1);
+                    }
+                    tmem_st32u(s_addr + h * 32, p);
+                };
+                probabilities(0, s0);
+                if (kFp8) load(1, s0);
+                probabilities(1, kFp8 ? s0 : s1);
                 l += (l0 + l1) + (l2 + l3);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) arrive_leader_relaxed(&sh->p_full[buf]);
             }
-            asm volatile("bar.sync 2, 256;" ::: "memory");  // the maxima have been read
-            sh->half[half][rl] = l;
-            asm volatile("bar.sync 2, 256;" ::: "memory");
-            l += sh->half[half ^ 1][rl];
             // O of the whole item
-            await(&sh->o_full, n & 1);
+            if (!ok || !await(&sh->o_full, n & 1)) break;
             ++n;
-            const bool mine = ok && r / kGrp < it.g.nq && r < kTcRows, none = l == 0.f;
+            const bool mine = r / kGrp < it.g.nq && r < kTcRows, none = l == 0.f;
             const float inv = none ? 0.f : 1.f / l;
             const bool complete = it.i0 == 0 && it.i1 == it.g.nt;
             const int64_t piece = 2 * worker + (it.i0 == 0 ? 1 : 0);
             const int64_t row = (it.g.row0 + r / kGrp) * kHQ + it.hd * kGrp + r % kGrp;
 #pragma unroll 1
-            for (int c = half * 4; c < half * 4 + 4; ++c) {
+            for (int c = 0; c < kD / 32; ++c) {
                 float o[32];
                 tmem_ld32(lane_addr + kTcO + c * 32, o);
                 tmem_wait_ld();
@@ -663,7 +712,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_leader_relaxed(&sh->o_empty);
-            if (mine && half == 0) {
+            if (mine) {
                 const float lse2 = none ? -INFINITY : m + log2f(l);
                 if (!complete) a.ws[2 * workers * kTcRows * kD + piece * kTcRows + r] = lse2;
                 else if (a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
@@ -671,102 +720,88 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
         }
     } else if (kFp8) {
         // ---------------- e4m3 codes to bf16 ----------------
-        TcTable *tab = reinterpret_cast<TcTable *>(smem + C::kOffTable);
-        const int ct = threadIdx.x - 384, cw = ct >> 5, k8 = lane >> 2, piece = lane & 3;
+        const TcTable *tab = reinterpret_cast<const TcTable *>(smem + C::kOffTable);
+        const int cw = warp - 8, k8 = lane >> 2, piece = lane & 3;
         const uint32_t ring_u = smem_u32(ring);
-        const uint8_t *kp = static_cast<const uint8_t *>(a.pool.k), *vp = static_cast<const uint8_t *>(a.pool.v);
-        uint32_t stage = 0, ph = 1;
-        while (it.next(a)) {  // to the end also after a wait that gave up: the four warps meet at barriers
-            const int nt = it.i1 - it.i0;
-            auto scale_byte = [&](const uint8_t *sc, int32_t row) -> uint32_t {
-                return row >= 0 ? __ldg(sc + row) : 127u;
-            };
-            auto put = [&](int i, int32_t row, uint32_t kb, uint32_t vb) {
-                tab->row[i % 3][ct] = row;
-                tab->ks[i % 3][ct] = (uint8_t)kb;
-                tab->vs[i % 3][ct] = (uint8_t)vb;
-            };
-            uint4 kreg[8], vreg[8];
-            uint32_t kb[2], vb[4];
-            auto load_k = [&](int i) {
+        const uint8_t *kp = static_cast<const uint8_t *>(a.pool.k) + piece * 16;
+        const uint8_t *vp = static_cast<const uint8_t *>(a.pool.v) + rank * 128 + piece * 16;
+        uint32_t stage = 0, ph = 1, n = 0;
+        // A warp converts 8 keys of K (all dims) and 16 of V (this CTA's dims) per tile; the next
+        // half tile of the other kind is loaded before one is converted.
+        uint4 kreg[4], vreg[4];
+        uint32_t kb, vb[2];
+        auto load_k = [&](uint32_t x) {
+            const int key = (int)rank * 64 + cw * 8 + k8;
+            const int32_t row = tab->row[x][key];
+            kb = tab->ks[x][key];
+            const uint8_t *src = kp + (int64_t)row * kD;
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int key = (int)rank * 64 + cw * 16 + q * 8 + k8;
-                    const int32_t row = tab->row[i % 3][key];
-                    kb[q] = tab->ks[i % 3][key];
-                    const uint8_t *src = kp + (int64_t)row * kD + piece * 16;
+            for (int c = 0; c < 4; ++c)
+                kreg[c] = row >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        auto load_v = [&](uint32_t x) {
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        kreg[q * 4 + c] = row >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
-                }
-            };
-            auto load_v = [&](int i) {
+            for (int q = 0; q < 2; ++q) {
+                const int key = cw * 16 + q * 8 + k8;
+                const int32_t row = tab->row[x][key];
+                vb[q] = tab->vs[x][key];
+                const uint8_t *src = vp + (int64_t)row * kD;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int key = cw * 32 + q * 8 + k8;
-                    const int32_t row = tab->row[i % 3][key];
-                    vb[q] = tab->vs[i % 3][key];
-                    const uint8_t *src = vp + (int64_t)row * kD + rank * 128 + piece * 16;
+                for (int c = 0; c < 2; ++c)
+                    vreg[q * 2 + c] = row >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
+            }
+        };
+        auto table_ready = [&](uint32_t t) -> bool {
+            ok = mbar_wait(&sh->tab_full[t % kTcTables], (t / kTcTables) & 1, abort_flag);
+            return ok = __all_sync(0xffffffffu, ok);
+        };
+        auto slot_ready = [&]() -> bool {
+            ok = mbar_wait(&sh->kv_empty[stage], ph, abort_flag);
+            return ok = __all_sync(0xffffffffu, ok);
+        };
+        auto slot_done = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh->kv_full[stage]);
+            if (++stage == C::kStages) {
+                stage = 0;
+                ph ^= 1u;
+            }
+        };
+        while (ok && it.next(a)) {
+            const uint32_t nt = (uint32_t)(it.i1 - it.i0);
+            if (!table_ready(n)) break;
+            load_k(n % kTcTables);
+            for (uint32_t i = 0; i <= nt; ++i) {
+                if (i < nt) {  // K(i)
+                    if (!slot_ready()) break;
+                    const RowScale sc = row_scale(kb);
+                    const uint32_t dst = ring_u + stage * kTcSlot + (cw * 8 + k8) * 128;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        vreg[q * 2 + c] = row >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
-                }
-            };
-            auto slot_ready = [&]() -> bool {
-                ok = ok && mbar_wait(&sh->kv_empty[stage], ph, abort_flag);
-                return ok = __all_sync(0xffffffffu, ok);
-            };
-            auto slot_done = [&]() {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh->kv_full[stage]);
-                if (++stage == C::kStages) {
-                    stage = 0;
-                    ph ^= 1u;
-                }
-            };
-            // the tables run ahead: tile i + 1's is written while tile i is converted, its scales were
-            // fetched one step earlier, its pages two
-            uint32_t off = 0u;
-            int32_t page = it.page_of(a, it.i0, ct, &off), row_b = it.row_of(a, page, off);
-            put(0, row_b, scale_byte(a.pool.k_scales, row_b), scale_byte(a.pool.v_scales, row_b));
-            page = it.page_of(a, it.i0 + 1, ct, &off);
-            row_b = it.row_of(a, page, off);
-            uint32_t nkb = scale_byte(a.pool.k_scales, row_b), nvb = scale_byte(a.pool.v_scales, row_b);
-            page = it.page_of(a, it.i0 + 2, ct, &off);
-            asm volatile("bar.sync 1, 128;" ::: "memory");
-            load_k(0);
-            for (int i = 0; i <= nt; ++i) {
-                put(i + 1, row_b, nkb, nvb);
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                row_b = it.row_of(a, page, off);
-                nkb = scale_byte(a.pool.k_scales, row_b);
-                nvb = scale_byte(a.pool.v_scales, row_b);
-                page = it.page_of(a, it.i0 + i + 3, ct, &off);
-                if (i < nt && slot_ready()) {  // K(i)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const RowScale sc = row_scale(kb[q]);
-                        const uint32_t dst = ring_u + stage * kTcSlot + (cw * 16 + q * 8 + k8) * 128;
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) codes_to_slot(kreg[q * 4 + c], sc, dst + c * kTcKChunk, 2 * piece, k8);
-                    }
+                    for (int c = 0; c < 4; ++c) codes_to_slot(kreg[c], sc, dst + c * kTcKChunk, 2 * piece, k8);
                     slot_done();
                 }
-                if (i + 1 < nt) load_k(i + 1);
-                if (i > 0 && slot_ready()) {  // V(i - 1)
+                if (i + 1 < nt) {
+                    if (!table_ready(n + i + 1)) break;
+                    load_k((n + i + 1) % kTcTables);
+                }
+                if (i > 0) {  // V(i - 1)
+                    if (!slot_ready()) break;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 2; ++q) {
                         const RowScale sc = row_scale(vb[q]);
-                        const uint32_t dst = ring_u + stage * kTcSlot + (cw * 32 + q * 8 + k8) * 128;
+                        const uint32_t dst = ring_u + stage * kTcSlot + (cw * 16 + q * 8 + k8) * 128;
 #pragma unroll
                         for (int c = 0; c < 2; ++c) codes_to_slot(vreg[q * 2 + c], sc, dst + c * kTcVChunk, 2 * piece, k8);
                     }
                     slot_done();
                 }
-                if (i < nt) load_v(i);
+                if (i < nt) {
+                    load_v((n + i) % kTcTables);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh->tab_empty[(n + i) % kTcTables]);
+                }
             }
-            // the next item's tables overwrite this one's
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            n += nt;
         }
     }
 
