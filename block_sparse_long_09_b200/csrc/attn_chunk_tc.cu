@@ -205,6 +205,57 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// two fp32 values at a time
+__device__ __forceinline__ uint64_t pack2(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t x)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// lane 4 x + q of every four lanes gives its v[j] to lane 4 x + j, which holds it as v[q]
+__device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane)
+{
+    auto swap = [&](uint4 &a, uint4 &b, int bit) {  // the lane with the bit sends a, the other b
+        const bool up = (lane & bit) != 0;
+        uint4 s = up ? a : b, r;
+        r.x = __shfl_xor_sync(0xffffffffu, s.x, bit);
+        r.y = __shfl_xor_sync(0xffffffffu, s.y, bit);
+        r.z = __shfl_xor_sync(0xffffffffu, s.z, bit);
+        r.w = __shfl_xor_sync(0xffffffffu, s.w, bit);
+        if (up) a = r; else b = r;
+    };
+    swap(v[0], v[1], 1);
+    swap(v[2], v[3], 1);
+    swap(v[0], v[2], 2);
+    swap(v[1], v[3], 2);
+}
+
 // The items of a share, in order: every role walks the same list.
 struct TcWalk {
     int64_t at, te, slot, first;
@@ -602,10 +653,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                 // unless every row sees every key of the tile: columns hi and below, from lo on or below sk
                 const bool edge = !(it.g.t0 >= 0 && j0 + kTcKeys - 1 <= it.g.t0 &&
                                     (a.window <= 0 || it.t_last - j0 < a.window || j0 + kTcKeys <= a.sinks));
-                const int64_t d64 = t - j0, w64 = a.window > 0 ? d64 - a.window + 1 : 0, k64 = a.sinks - j0;
-                const int hi = (int)(d64 < -1 ? -1 : (d64 > kTcKeys ? kTcKeys : d64));
-                const int lo = (int)(w64 < 0 ? 0 : (w64 > kTcKeys ? kTcKeys : w64));
-                const int sk = (int)(k64 < 0 ? 0 : (k64 > kTcKeys ? kTcKeys : k64));
+                int hi = kTcKeys, lo = 0, sk = 0;
+                if (edge) {
+                    const int64_t d = t - j0, w = a.window > 0 ? d - a.window + 1 : 0, k = a.sinks - j0;
+                    hi = (int)(d < -1 ? -1 : (d > kTcKeys ? kTcKeys : d));
+                    lo = (int)(w < 0 ? 0 : (w > kTcKeys ? kTcKeys : w));
+                    sk = (int)(k < 0 ? 0 : (k > kTcKeys ? kTcKeys : k));
+                }
                 auto load = [&](int h, float (&s)[kHalf]) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) tmem_ld32(s_addr + h * kHalf + c * 32, s + c * 32);
@@ -619,13 +673,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                 auto largest = [&](const float (&s)[kHalf]) -> float {
                     float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
 #pragma unroll
-                    for (int c = 4; c < kHalf; c += 4) {
-                        x0 = fmaxf(x0, s[c]);
-                        x1 = fmaxf(x1, s[c + 1]);
-                        x2 = fmaxf(x2, s[c + 2]);
-                        x3 = fmaxf(x3, s[c + 3]);
+                    for (int c = 4; c + 8 <= kHalf; c += 8) {
+                        x0 = max3(x0, s[c], s[c + 1]);
+                        x1 = max3(x1, s[c + 2], s[c + 3]);
+                        x2 = max3(x2, s[c + 4], s[c + 5]);
+                        x3 = max3(x3, s[c + 6], s[c + 7]);
                     }
-                    return fmaxf(fmaxf(x0, x1), fmaxf(x2, x3));
+                    x0 = max3(x0, s[kHalf - 4], s[kHalf - 3]);
+                    x1 = max3(x1, s[kHalf - 2], s[kHalf - 1]);
+                    return fmaxf(max3(x0, x1, x2), x3);
                 };
                 // The second half first, for its maximum: bf16 pools keep it in registers; with 16 warps
                 // there is no room for it, and it is read again below.
@@ -643,27 +699,28 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                     // O of the tiles before: T - 1 products have completed at least (S(T) came behind them)
                     if (!await(&sh->pv_done, (T - 1) & 1)) break;
 #pragma unroll 1
-                    for (int c = 0; c < kD / 16; ++c) {
-                        float o[16];
-                        tmem_ld16(lane_addr + kTcO + c * 16, o);
+                    for (int c = 0; c < kD / 32; ++c) {
+                        float o[32];
+                        tmem_ld32(lane_addr + kTcO + c * 32, o);
                         tmem_wait_ld();
-                        tmem_st16(lane_addr + kTcO + c * 16, o, f);
+                        tmem_st16(lane_addr + kTcO + c * 32, o, f);
+                        tmem_st16(lane_addr + kTcO + c * 32 + 16, o + 16, f);
                     }
                 }
                 if (m == -INFINITY) m = mx;
                 const float base = m == -INFINITY ? 0.f : m;
-                float l0 = 0.f, l1 = 0.f, l2 = 0.f, l3 = 0.f;
+                const uint64_t c22 = pack2(c2, c2), b22 = pack2(-base, -base);
+                uint64_t l01 = pack2(l, 0.f), l23 = pack2(0.f, 0.f);
                 // keys 64 h .. as columns 32 h ..: the scores there have been read by now
                 auto probabilities = [&](int h, const float (&s)[kHalf]) {
                     uint32_t p[32];
 #pragma unroll
                     for (int e = 0; e < 32; e += 2) {
-                        const float p0 = ex2(fmaf(s[2 * e], c2, -base)), p1 = ex2(fmaf(s[2 * e + 1], c2, -base));
-                        const float p2 = ex2(fmaf(s[2 * e + 2], c2, -base)), p3 = ex2(fmaf(s[2 * e + 3], c2, -base));
-                        l0 += p0;
-                        l1 += p1;
-                        l2 += p2;
-                        l3 += p3;
+                        const float2 x = unpack2(fma2(pack2(s[2 * e], s[2 * e + 1]), c22, b22));
+                        const float2 y = unpack2(fma2(pack2(s[2 * e + 2], s[2 * e + 3]), c22, b22));
+                        const float p0 = ex2(x.x), p1 = ex2(x.y), p2 = ex2(y.x), p3 = ex2(y.y);
+                        l01 = add2(l01, pack2(p0, p1));
+                        l23 = add2(l23, pack2(p2, p3));
                         const __nv_bfloat162 a0 = __floats2bfloat162_rn(p0, p1), a1 = __floats2bfloat162_rn(p2, p3);
                         p[e] = *reinterpret_cast<const uint32_t *>(&a0);
                         p[e + 1] = *reinterpret_cast<const uint32_t *>(&a1);
@@ -673,7 +730,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                 probabilities(0, s0);
                 if (kFp8) load(1, s0);
                 probabilities(1, kFp8 ? s0 : s1);
-                l += (l0 + l1) + (l2 + l3);
+                const float2 la = unpack2(add2(l01, l23));
+                l = la.x + la.y;
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -687,6 +745,9 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
             const bool complete = it.i0 == 0 && it.i1 == it.g.nt;
             const int64_t piece = 2 * worker + (it.i0 == 0 ? 1 : 0);
             const int64_t row = (it.g.row0 + r / kGrp) * kHQ + it.hd * kGrp + r % kGrp;
+            // four lanes exchange 16-byte pieces of their four rows, so that a store writes 64 bytes of each
+            const int r4 = r & ~3, q = lane & 3;
+            const int rows = it.g.nq * kGrp - r4;  // of the four, those that are written
 #pragma unroll 1
             for (int c = 0; c < kD / 32; ++c) {
                 float o[32];
@@ -694,19 +755,35 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] = none ? 0.f : o[e] * inv;
-                if (!mine) continue;
                 if (complete) {
+                    uint4 v[4];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
+                    for (int e = 0; e < 4; ++e) {
                         __nv_bfloat162 h[4];
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) h[x] = __floats2bfloat162_rn(o[e + 2 * x], o[e + 2 * x + 1]);
-                        *reinterpret_cast<uint4 *>(a.o + row * kD + c * 32 + e) = *reinterpret_cast<const uint4 *>(h);
+                        for (int x = 0; x < 4; ++x) h[x] = __floats2bfloat162_rn(o[e * 8 + 2 * x], o[e * 8 + 2 * x + 1]);
+                        v[e] = *reinterpret_cast<const uint4 *>(h);
                     }
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(a.ws + (piece * kTcRows + r) * kD + c * 32);
+                    transpose4(v, lane);
+                    // (the four rows are heads of one token: 12 is a multiple of 4)
+                    __nv_bfloat16 *dst = a.o + (row - q) * kD + c * 32 + q * 8;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    for (int j = 0; j < 4; ++j)
+                        if (j < rows) *reinterpret_cast<uint4 *>(dst + j * kD) = v[j];
+                } else {
+                    float *dst = a.ws + (piece * kTcRows + r4) * kD + c * 32 + q * 4;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = make_uint4(__float_as_uint(o[h * 16 + 4 * e]), __float_as_uint(o[h * 16 + 4 * e + 1]),
+                                              __float_as_uint(o[h * 16 + 4 * e + 2]), __float_as_uint(o[h * 16 + 4 * e + 3]));
+                        transpose4(v, lane);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j < rows) *reinterpret_cast<uint4 *>(dst + j * kD + h * 16) = v[j];
+                    }
                 }
             }
             tc_fence_before();

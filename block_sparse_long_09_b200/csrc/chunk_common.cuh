@@ -261,18 +261,87 @@ chunk_merge_kernel(const ChunkArgs a, const int64_t *__restrict__ prefix, int64_
     }
 }
 
+// The same for many rows and few pieces each: a warp per kPer rows, in one pass over the pieces.
+template <int kTok, int kKeys, int kPer>
+__global__ void __launch_bounds__(kMergeThreads)
+chunk_merge_many_kernel(const ChunkArgs a, const int64_t *__restrict__ prefix, int64_t workers)
+{
+    constexpr int kRows = kTok * kGrp;
+    pdl_enter();
+    const int64_t slot = blockIdx.x >> 1;
+    const int hd = blockIdx.x & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t slots = chunk_slots<kTok>(a.total_q, a.batch);
+    const int64_t total = prefix[slots], p0 = prefix[slot], p1 = prefix[slot + 1];
+    const int64_t nt = (p1 - p0) >> 1, rs = p0 + hd * nt, re = rs + nt;
+    int64_t c0 = 0, last = -1;
+    if (nt > 0) {
+        c0 = ((rs + 1) * workers - 1) / total;  // the share that holds the item's first tile
+        if (share_start(c0 + 1, total, workers) >= re) return;  // finished by one worker
+        last = (re * workers - 1) / total;      // and its last one
+    }
+    const ChunkGroup g = chunk_group<kTok, kKeys>(a, slot);
+    const int rows = g.nq * kGrp, r0 = (blockIdx.y * kMergeWarps + warp) * kPer;
+    if (r0 >= rows) return;
+    const float *lse = a.ws + 2 * workers * kRows * kD;
+    float mx[kPer], sum[kPer], acc[kPer][8];
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        mx[u] = -INFINITY;
+        sum[u] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[u][j] = 0.f;
+    }
+    for (int64_t c = c0; c <= last; ++c) {
+        if (c != c0 && share_start(c + 1, total, workers) == share_start(c, total, workers)) continue;  // an empty share
+        const int64_t p = c == c0 ? 2 * c0 + 1 : 2 * c;
+        float w[kPer], x[kPer][8];
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const int64_t at = p * kRows + (r0 + u < rows ? r0 + u : r0);
+            w[u] = lse[at];
+            const float4 *src = reinterpret_cast<const float4 *>(a.ws + at * kD + lane * 8);
+            *reinterpret_cast<float4 *>(&x[u][0]) = __ldcs(src);
+            *reinterpret_cast<float4 *>(&x[u][4]) = __ldcs(src + 1);
+        }
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const float m = fmaxf(mx[u], w[u]), base = m == -INFINITY ? 0.f : m;
+            const float f = exp2f(mx[u] - base), e = exp2f(w[u] - base);
+            mx[u] = m;
+            sum[u] = fmaf(sum[u], f, e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[u][j] = fmaf(acc[u][j], f, e * x[u][j]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+        const int r = r0 + u;
+        if (r >= rows) break;
+        const bool none = sum[u] == 0.f;
+        const float inv = none ? 0.f : 1.f / sum[u];
+        const int64_t row = (g.row0 + r / kGrp) * kHQ + hd * kGrp + r % kGrp;
+        __nv_bfloat162 h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            h[j] = __floats2bfloat162_rn(none ? 0.f : acc[u][2 * j] * inv, none ? 0.f : acc[u][2 * j + 1] * inv);
+        *reinterpret_cast<uint4 *>(a.o + row * kD + lane * 8) = *reinterpret_cast<const uint4 *>(h);
+        if (a.lse != nullptr && lane == 0) a.lse[row] = none ? -INFINITY : (mx[u] + log2f(sum[u])) * 0.6931471805599453f;
+    }
+}
+
 template <int kTok, int kKeys>
 cudaError_t launch_chunk_merge(const ChunkArgs &a, const int64_t *prefix, int64_t workers, cudaStream_t stream)
 {
     constexpr int kRows = kTok * kGrp;
     const int64_t items = 2 * chunk_slots<kTok>(a.total_q, a.batch);
     if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    // few rows: a CTA per row, its eight warps over the row's pieces; many: a warp per row
+    // few rows: a CTA per row, its eight warps over the row's pieces; many: a warp per four rows
     if (items * kRows <= 4096)
         return launch_pdl(chunk_merge_kernel<kTok, kKeys, 8>, dim3((unsigned)items, kRows), dim3(kMergeThreads), 0,
                           stream, a, prefix, workers);
-    return launch_pdl(chunk_merge_kernel<kTok, kKeys, 1>, dim3((unsigned)items, (kRows + 7) / 8), dim3(kMergeThreads), 0,
-                      stream, a, prefix, workers);
+    constexpr int kPer = 4, kBlock = kMergeWarps * kPer;
+    return launch_pdl(chunk_merge_many_kernel<kTok, kKeys, kPer>, dim3((unsigned)items, (kRows + kBlock - 1) / kBlock),
+                      dim3(kMergeThreads), 0, stream, a, prefix, workers);
 }
 
 }  // namespace
