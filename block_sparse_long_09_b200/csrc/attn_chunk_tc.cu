@@ -50,7 +50,7 @@ struct TcShared {
     uint64_t tab_full[kTcTables], tab_empty[kTcTables];
     uint32_t tmem_base;
     int abort_flag;
-    int64_t scan[16];
+    int64_t scan[16], walk[16][3];
     ChunkShare share;
 };
 
@@ -171,16 +171,13 @@ __device__ __forceinline__ void commit_both(uint64_t *bar)
         ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t *v)
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t *v)
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
-        " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16,"
-        " %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0],"
+        " {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
         ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
-          "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]),
-          "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+          "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
 
@@ -258,20 +255,33 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane)
 
 // The items of a share, in order: every role walks the same list.
 struct TcWalk {
-    int64_t at, te, slot, first;
+    const ChunkShare *share;
+    int64_t *state;  // shared memory, of this warp: next tile, its group's slot and that slot's first tile
     // the current item
-    ChunkGroup g;
+    int s, nq, nt, ns, w_tile;  // as in its ChunkGroup
+    int row0, t0;
     int hd, i0, i1;
     int t_first, t_last;  // positions of the first (at least 0) and the last token
     int near, sinks;      // some row sees the keys near .. t_last and those below sinks
     const int32_t *table; // the sequence's row of the block table
 
-    __device__ __forceinline__ explicit TcWalk(const ChunkShare &s) : at(s.ts), te(s.te), slot(s.slot), first(s.first) {}
+    __device__ __forceinline__ TcWalk(const ChunkShare *sh, int64_t *st) : share(sh), state(st)
+    {
+        if ((threadIdx.x & 31) == 0) {
+            st[0] = sh->ts;
+            st[1] = sh->slot;
+            st[2] = sh->first;
+        }
+        __syncwarp();
+    }
 
+    // by one lane or by all lanes of the warp together
     __device__ __forceinline__ bool next(const ChunkArgs &a)
     {
+        int64_t at = state[0], slot = state[1], first = state[2];
+        const int64_t te = share->te;
         if (at >= te) return false;
-        g = chunk_group<kTcTok, kTcKeys>(a, slot);
+        ChunkGroup g = chunk_group<kTcTok, kTcKeys>(a, slot);
         while (at >= first + 2 * (int64_t)g.nt) {  // empty slots between two groups
             first += 2 * (int64_t)g.nt;
             g = chunk_group<kTcTok, kTcKeys>(a, ++slot);
@@ -280,14 +290,28 @@ struct TcWalk {
         const int64_t item = first + (int64_t)hd * g.nt;
         i0 = (int)(at - item);
         i1 = te - item < g.nt ? (int)(te - item) : g.nt;
-        at = item + i1;
-        t_first = g.t0 > 0 ? (int)g.t0 : 0;
-        t_last = (int)(g.t0 + g.nq - 1);
+        s = g.s;
+        nq = g.nq;
+        nt = g.nt;
+        ns = g.ns;
+        w_tile = (int)g.w_tile;
+        row0 = (int)g.row0;
+        t0 = (int)g.t0;
+        t_first = t0 > 0 ? t0 : 0;
+        t_last = t0 + nq - 1;
         near = a.window > 0 ? t_first - (int)a.window + 1 : 0;
         sinks = (int)a.sinks;
-        table = a.pool.table + (int64_t)g.s * a.pool.max_pages;
+        table = a.pool.table + (int64_t)s * a.pool.max_pages;
+        __syncwarp(__activemask());
+        state[0] = item + i1;  // (the same values from every lane)
+        state[1] = slot;
+        state[2] = first;
+        __syncwarp(__activemask());
         return true;
     }
+
+    // first key of tile i
+    __device__ __forceinline__ int tile(int i) const { return (i < ns ? i : w_tile + (i - ns)) * kTcKeys; }
 
     // does any row of the item see key j
     __device__ __forceinline__ bool any_sees(int j) const
@@ -301,7 +325,7 @@ struct TcWalk {
     __device__ __forceinline__ int32_t page_of(const ChunkArgs &a, int i, int key, uint32_t *off) const
     {
         if (i >= i1) return kUnseen;
-        const int j = (i < g.ns ? i : (int)g.w_tile + (i - g.ns)) * kTcKeys + key;
+        const int j = tile(i) + key;
         if (!any_sees(j)) return kUnseen;
         const uint32_t p = a.pool.page_of((uint32_t)j, off);
         return p < (uint32_t)a.pool.max_pages ? __ldg(table + p) : kNoPage;
@@ -414,7 +438,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
     tc_fence_after();
     const uint32_t tmem = sh->tmem_base;
     volatile int *abort_flag = &sh->abort_flag;
-    TcWalk it(sh->share);
+    TcWalk it(&sh->share, sh->walk[warp]);
     bool ok = true;
     if (warp == 0) {
         // ---------------- Q ----------------
@@ -425,7 +449,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
             if (lane == 0) mbar_arrive_expect_tx(&sh->q_full, kTcQ);
             __syncwarp();
             const int row = (int)rank * 128 + lane * 4, tok = row / kGrp;
-            const int32_t y = tok < it.g.nq ? (int32_t)(it.g.row0 + tok) : (int32_t)a.total_q;  // outside: zeros
+            const int32_t y = tok < it.nq ? (int32_t)(it.row0 + tok) : (int32_t)a.total_q;  // outside: zeros
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 tma_load_3d(sQ + c * kTcQChunk + lane * 512, &map_q, &sh->q_full, c * 64, it.hd * kGrp + row % kGrp, y);
@@ -632,7 +656,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
         }
     } else if (warp < 8) {
         // ---------------- softmax and epilogue ----------------
-        constexpr int kHalf = kTcKeys / 2;
+        constexpr int kPart = kTcKeys / 2;
         const int quad = warp & 3, rl = quad * 32 + lane, r = (int)rank * 128 + rl;
         const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
         const float c2 = a.scale * 1.4426950408889634f;
@@ -644,52 +668,62 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
             return ok;
         };
         while (ok && it.next(a)) {
-            const int64_t t = it.g.t0 + r / kGrp;  // this row's position (rows past the tokens: not written)
+            const int t = it.t0 + r / kGrp;  // this row's position (rows past the tokens: not written)
             float m = -INFINITY, l = 0.f;          // running maximum of c2 s, sum of exp2(c2 s - m)
             for (int i = it.i0; i < it.i1; ++i, ++T) {
                 const uint32_t buf = T & 1, s_addr = lane_addr + buf * kTcKeys;
                 if (!await(&sh->s_full[buf], (T >> 1) & 1)) break;
-                const int64_t j0 = tile_start(it.g, i, kTcKeys);
+                const int j0 = it.tile(i);
                 // unless every row sees every key of the tile: columns hi and below, from lo on or below sk
-                const bool edge = !(it.g.t0 >= 0 && j0 + kTcKeys - 1 <= it.g.t0 &&
+                const bool edge = !(j0 + kTcKeys - 1 <= it.t0 &&
                                     (a.window <= 0 || it.t_last - j0 < a.window || j0 + kTcKeys <= a.sinks));
                 int hi = kTcKeys, lo = 0, sk = 0;
                 if (edge) {
-                    const int64_t d = t - j0, w = a.window > 0 ? d - a.window + 1 : 0, k = a.sinks - j0;
-                    hi = (int)(d < -1 ? -1 : (d > kTcKeys ? kTcKeys : d));
-                    lo = (int)(w < 0 ? 0 : (w > kTcKeys ? kTcKeys : w));
-                    sk = (int)(k < 0 ? 0 : (k > kTcKeys ? kTcKeys : k));
+                    hi = t - j0;
+                    lo = a.window > 0 && a.window <= hi ? hi - (int)a.window + 1 : 0;
+                    sk = it.sinks - j0;
                 }
-                auto load = [&](int h, float (&s)[kHalf]) {
+                auto load = [&](int h, float (&s)[kPart]) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) tmem_ld32(s_addr + h * kHalf + c * 32, s + c * 32);
-                    tmem_wait_ld();
+                    for (int c = 0; c < kPart / 32; ++c) tmem_ld32(s_addr + h * kPart + c * 32, s + c * 32);
+                };
+                auto mask = [&](int h, float (&s)[kPart]) {
                     if (edge) {
 #pragma unroll
-                        for (int c = 0; c < kHalf; ++c)
-                            if (h * kHalf + c > hi || (h * kHalf + c < lo && h * kHalf + c >= sk)) s[c] = -INFINITY;
+                        for (int c = 0; c < kPart; ++c)
+                            if (h * kPart + c > hi || (h * kPart + c < lo && h * kPart + c >= sk)) s[c] = -INFINITY;
                     }
                 };
-                auto largest = [&](const float (&s)[kHalf]) -> float {
-                    float x0 = s[0], x1 = s[1], x2 = s[2], x3 = s[3];
+                auto largest = [&](float x, const float (&s)[kPart]) -> float {
+                    float y = s[0], z = s[1], w = s[2];
+                    x = fmaxf(x, s[3]);
 #pragma unroll
-                    for (int c = 4; c + 8 <= kHalf; c += 8) {
-                        x0 = max3(x0, s[c], s[c + 1]);
-                        x1 = max3(x1, s[c + 2], s[c + 3]);
-                        x2 = max3(x2, s[c + 4], s[c + 5]);
-                        x3 = max3(x3, s[c + 6], s[c + 7]);
+                    for (int c = 4; c + 8 <= kPart; c += 8) {
+                        x = max3(x, s[c], s[c + 1]);
+                        y = max3(y, s[c + 2], s[c + 3]);
+                        z = max3(z, s[c + 4], s[c + 5]);
+                        w = max3(w, s[c + 6], s[c + 7]);
                     }
-                    x0 = max3(x0, s[kHalf - 4], s[kHalf - 3]);
-                    x1 = max3(x1, s[kHalf - 2], s[kHalf - 1]);
-                    return fmaxf(max3(x0, x1, x2), x3);
+                    x = max3(x, s[kPart - 4], s[kPart - 3]);
+                    y = max3(y, s[kPart - 2], s[kPart - 1]);
+                    return fmaxf(max3(x, y, z), w);
                 };
-                // The second half first, for its maximum: bf16 pools keep it in registers; with 16 warps
-                // there is no room for it, and it is read again below.
-                float s0[kHalf], s1[kHalf];
+                // The maximum first.  bf16 pools keep all scores in registers from here on; with 16 warps
+                // there is room for the first half only, and the second is read again below.
+                float s0[kPart], s1[kPart];
+                float mx = -INFINITY;
                 load(1, s1);
-                float mx = largest(s1);
-                load(0, s0);
-                mx = fmaxf(mx, largest(s0)) * c2;
+                if (!kFp8) load(0, s0);
+                tmem_wait_ld();
+                mask(1, s1);
+                mx = largest(mx, s1);
+                if (kFp8) {
+                    load(0, s0);
+                    tmem_wait_ld();
+                }
+                mask(0, s0);
+                mx = largest(mx, s0);
+                mx *= c2;
                 // O and l are zero until a key is visible, rescaled after that
                 const bool grow = m != -INFINITY && mx > m + kTcRescale;
                 if (__any_sync(0xffffffffu, grow)) {
@@ -711,24 +745,32 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                 const float base = m == -INFINITY ? 0.f : m;
                 const uint64_t c22 = pack2(c2, c2), b22 = pack2(-base, -base);
                 uint64_t l01 = pack2(l, 0.f), l23 = pack2(0.f, 0.f);
-                // keys 64 h .. as columns 32 h ..: the scores there have been read by now
-                auto probabilities = [&](int h, const float (&s)[kHalf]) {
-                    uint32_t p[32];
+                // half h's keys as columns 32 h ..: the scores there have been read by now
+                auto probabilities = [&](int h, const float (&s)[kPart]) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float2 x = unpack2(fma2(pack2(s[2 * e], s[2 * e + 1]), c22, b22));
-                        const float2 y = unpack2(fma2(pack2(s[2 * e + 2], s[2 * e + 3]), c22, b22));
-                        const float p0 = ex2(x.x), p1 = ex2(x.y), p2 = ex2(y.x), p3 = ex2(y.y);
-                        l01 = add2(l01, pack2(p0, p1));
-                        l23 = add2(l23, pack2(p2, p3));
-                        const __nv_bfloat162 a0 = __floats2bfloat162_rn(p0, p1), a1 = __floats2bfloat162_rn(p2, p3);
-                        p[e] = *reinterpret_cast<const uint32_t *>(&a0);
-                        p[e + 1] = *reinterpret_cast<const uint32_t *>(&a1);
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            const int c = 32 * x + 2 * e;
+                            const float2 y = unpack2(fma2(pack2(s[c], s[c + 1]), c22, b22));
+                            const float2 z = unpack2(fma2(pack2(s[c + 2], s[c + 3]), c22, b22));
+                            const float p0 = ex2(y.x), p1 = ex2(y.y), p2 = ex2(z.x), p3 = ex2(z.y);
+                            l01 = add2(l01, pack2(p0, p1));
+                            l23 = add2(l23, pack2(p2, p3));
+                            const __nv_bfloat162 a0 = __floats2bfloat162_rn(p0, p1), a1 = __floats2bfloat162_rn(p2, p3);
+                            p[e] = *reinterpret_cast<const uint32_t *>(&a0);
+                            p[e + 1] = *reinterpret_cast<const uint32_t *>(&a1);
+                        }
+                        tmem_st16u(s_addr + h * 32 + x * 16, p);
                     }
-                    tmem_st32u(s_addr + h * 32, p);
                 };
                 probabilities(0, s0);
-                if (kFp8) load(1, s0);
+                if (kFp8) {
+                    load(1, s0);
+                    tmem_wait_ld();
+                    mask(1, s0);
+                }
                 probabilities(1, kFp8 ? s0 : s1);
                 const float2 la = unpack2(add2(l01, l23));
                 l = la.x + la.y;
@@ -740,14 +782,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
             // O of the whole item
             if (!ok || !await(&sh->o_full, n & 1)) break;
             ++n;
-            const bool mine = r / kGrp < it.g.nq && r < kTcRows, none = l == 0.f;
+            const bool mine = r / kGrp < it.nq && r < kTcRows, none = l == 0.f;
             const float inv = none ? 0.f : 1.f / l;
-            const bool complete = it.i0 == 0 && it.i1 == it.g.nt;
+            const bool complete = it.i0 == 0 && it.i1 == it.nt;
             const int64_t piece = 2 * worker + (it.i0 == 0 ? 1 : 0);
-            const int64_t row = (it.g.row0 + r / kGrp) * kHQ + it.hd * kGrp + r % kGrp;
+            const int64_t row = (int64_t)(it.row0 + r / kGrp) * kHQ + it.hd * kGrp + r % kGrp;
             // four lanes exchange 16-byte pieces of their four rows, so that a store writes 64 bytes of each
             const int r4 = r & ~3, q = lane & 3;
-            const int rows = it.g.nq * kGrp - r4;  // of the four, those that are written
+            const int rows = it.nq * kGrp - r4;  // of the four, those that are written
 #pragma unroll 1
             for (int c = 0; c < kD / 32; ++c) {
                 float o[32];

@@ -52,7 +52,7 @@ def test_lengths(qsa, page, lens_q, lens_k, fp8):
 
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (2, 3), (64, 0), (100, 4), (129, 200), (1000, 16), (5000, 7),
-                                          (63, 64), (128, 65)])
+                                          (63, 64), (128, 65), (2 ** 31 - 1, 5), (3, 2 ** 31 - 1)])
 @pytest.mark.parametrize("page,lens_q,lens_k", [(16, [1, 1, 1], [1, 500, 1300]), (12, [4, 3], [800, 130]),
                                                 (64, [150, 1], [701, 90]), (32, [64, 33], [64, 901])])
 def test_windows(qsa, page, lens_q, lens_k, window, sinks, fp8):
