@@ -1,52 +1,47 @@
-// attn_chunk.cu -- attention of the new tokens of every sequence over its paged cache,
-// rows kernel: up to kTok new tokens (12 kTok query rows of a KV head) per item.
+// attn_chunk.cu -- attention of the new tokens of every sequence over its paged cache:
+// the kernel for single new tokens (decoding), and the choice between the two kernels.
 //
-//   o[t, h] = sum_j p_j v[j, g] / sum_j p_j,  p_j = exp(scale <q[t, h], k[j, g]> - m)
+//   o[h] = sum_j p_j v[j, g] / sum_j p_j,  p_j = exp2(c2 <q[h], k[j, g]> - m)     c2 = scale log2(e)
 // over the cached positions j <= t with t - j < window or j < sinks (no window: all).
 //
-// One decoded token brings 12 rows to 512 B (e4m3) or 1 KB (bf16) of K and V per key, so this
-// kernel is bound by HBM; it is built to keep 64 KB of loads per CTA in flight, two CTAs per
-// SM, with nothing between memory and the matrix instructions but registers:
-//   * S = Q K^T by mma.m16n8k16: a warp takes 16 (e4m3) or 8 (bf16) keys of the tile, its
-//     lanes load 16 B pieces of the keys' rows straight into B fragments.  The order of the
-//     256 dims inside the sums is free, so it is chosen to make a lane's dims contiguous,
-//     and Q is laid out once per item in the same order (A fragments in shared memory).
+// One decoded token brings 12 rows to 512 B (e4m3) or 1 KB (bf16) of K and V per key: bound by
+// HBM, 22 or 43 cycles of an SM per key.  So nothing may interrupt the loads: a CTA per SM, whose
+// eight warps work alone.  Of every tile of 128 keys a warp takes 16, copies their K and V into a ring
+// of its own (16-byte asynchronous copies, 130 KB on their way per SM, zeros for keys that the
+// row does not see), and keeps its own running maximum, sum and all 256 dims of O in registers.
+// There is no barrier until the item ends, where the eight states are added up.  (A CTA-wide softmax
+// with K and V in registers reached 39 % of the copy rate: it waited at two barriers per tile.)
+//   * S = Q K^T and O += P V by mma.m16n8k16, the twelve heads in 16 rows.  S's accumulators are
+//     P's operand as they are; the order of the 256 dims inside S, of the dims of O and of a
+//     warp's 16 keys is free, and chosen so that a lane's loads are 16 contiguous bytes
+//     without bank conflicts (rows of the ring are padded by 16 or 32 bytes for that).
 //   * e4m3 codes become bf16 by moving their 7 low bits to the top of a bf16 and
 //     multiplying by 2^120; exact.  The keys' scales multiply S, the values' scales multiply P:
-//     powers of two, exact as well.
-//   * the softmax statistics are shared through 8 row maxima in shared memory; P goes to
-//     shared memory as bf16 (its rounding: 2^-9 relative per term, as in every attention
+//     powers of two, exact as well (P rounds to bf16: 2^-9 relative, as in every attention
 //     kernel of this library).
-//   * O += P V: a warp owns 32 of the 256 dims for all the tile's keys.  Its lanes load 4
-//     dims of 4 consecutive keys; byte permutes pair the keys for the B fragments, so V
-//     needs no transpose through shared memory.
-// The next tile's K loads are issued as soon as S is computed, its pool rows two tiles ahead.
-// Tiles that no row sees are never read, and keys that no row of the item sees (behind the
-// sequence's end, before the window) are replaced by zeros, whatever their memory holds.
+//   * O is rescaled only when a row's maximum grows by more than 2^8.
 #include "chunk_common.cuh"
 
 namespace qsa {
 
 namespace {
 
-constexpr int kRowWarps = 8, kRowThreads = kRowWarps * 32;
+constexpr int kDecWarps = 8, kDecThreads = kDecWarps * 32, kDecKeys = 16 * kDecWarps;
 
 template <bool kFp8>
-struct RowCfg {
-    static constexpr int kKeys = kFp8 ? 128 : 64;         // keys per tile: 64 KB of K and V
-    static constexpr int kNT = kKeys / (8 * kRowWarps);   // 8-key column tiles of a warp's S
-    static constexpr int kPieces = kFp8 ? 4 : 8;          // 16 B pieces of a key's row per lane
-    static constexpr int kKS = kKeys / 16;                // k steps of P V
-    static constexpr int kPitch = kKeys + 8;              // P row pitch: ldmatrix without bank conflicts
+struct DecCfg {
+    static constexpr int kRow = kFp8 ? kD : 2 * kD;                  // bytes of a key's row of one KV head
+    static constexpr int kPitchK = kRow + 16, kPitchV = kRow + (kFp8 ? 32 : 16);
+    static constexpr int kSlot = 16 * kPitchV;                       // K or V of 16 keys
+    static constexpr int kAhead = kFp8 ? 2 : 1;                      // tiles on their way beside the current one
+    static constexpr int kRing = 2 * kAhead + 1;
+    static constexpr int kOffRing = 16 * 32 * 16;                    // behind Q's fragments
+    static constexpr int kMergePitch = kD + 4;                       // floats per row of a warp's state
+    static constexpr int kOffStats = kOffRing + kDecWarps * kRing * kSlot;
+    static constexpr int kSmem = kOffStats + 2 * kDecWarps * 16 * (int)sizeof(float);
+    static_assert(kDecWarps * kGrp * kMergePitch * 4 <= kDecWarps * kRing * kSlot, "the merge reuses the ring");
+    static_assert(kSmem <= 232448 - 1024, "shared memory of one CTA");
 };
-
-__device__ __forceinline__ uint4 ld_stream16(const void *p)
-{
-    uint4 r;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
-    return r;
-}
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1)
 {
@@ -57,380 +52,383 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint4 &a, uint32_
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 ldmatrix4(uint32_t addr)
+__device__ __forceinline__ uint4 ldmatrix4t(uint32_t addr)
 {
     uint4 r;
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr));
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr) : "memory");
     return r;
 }
 
-// two codes in the high bytes of a register's halves -> bf16 pair
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t x)
+__device__ __forceinline__ uint4 lds16(uint32_t addr)
 {
-    const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y),
-                                     __halves2bfloat162(__ushort_as_bfloat16(0x7B80), __ushort_as_bfloat16(0x7B80)));
-    return *reinterpret_cast<const uint32_t *>(&r);
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(addr) : "memory");
+    return r;
 }
 
-// kMT 16-row tiles of (token, head) rows: 1 token in 16, or 4 tokens in 48
-template <int kMT>
-constexpr int row_tokens() { return kMT * 16 / kGrp; }
-
-template <int kMT, bool kFp8>
-struct RowShared {
-    uint4 q[kMT][16][32];                                        // A fragments of Q
-    __nv_bfloat16 p[kMT * 16][RowCfg<kFp8>::kPitch];
-    float wmax[kRowWarps][kMT * 16], wsum[kRowWarps][kMT * 16];
-    alignas(16) int32_t row[3][RowCfg<kFp8>::kKeys];             // pool rows of the tiles' keys, -1: none
-    float ks[2][RowCfg<kFp8>::kKeys], vs[2][RowCfg<kFp8>::kKeys];
-    int64_t scan[kRowWarps];
-    ChunkShare share;
-};
-
-template <int kMT, bool kFp8>
-__global__ void __launch_bounds__(kRowThreads, 2)
-chunk_rows_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
+// four codes -> the bf16 pairs of codes (0, 1) and (2, 3)
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t &p01, uint32_t &p23)
 {
-    using C = RowCfg<kFp8>;
-    constexpr int kKeys = C::kKeys, kTok = row_tokens<kMT>(), kRows = kTok * kGrp;
-    constexpr int kBytes = kFp8 ? kD : 2 * kD;  // of a key's row of one KV head
-    __shared__ RowShared<kMT, kFp8> sh;
+    const uint32_t hi = (w & 0x80808080u) | ((w >> 4) & 0x07070707u), lo = (w << 4) & 0xF0F0F0F0u;
+    const __nv_bfloat162 up = __halves2bfloat162(__ushort_as_bfloat16(0x7B80), __ushort_as_bfloat16(0x7B80));  // 2^120
+    const uint32_t a = __byte_perm(lo, hi, 0x5140), b = __byte_perm(lo, hi, 0x7362);
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), up);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&b), up);
+    p01 = *reinterpret_cast<const uint32_t *>(&x);
+    p23 = *reinterpret_cast<const uint32_t *>(&y);
+}
+
+__device__ __forceinline__ float dec_ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(kDecThreads, 1)
+chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
+{
+    using C = DecCfg<kFp8>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ ChunkShare share;
+    __shared__ int64_t scan[kDecWarps];
     pdl_enter();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n = lane >> 2, c = lane & 3;      // fragment coordinates
-    chunk_share<kTok, kKeys, kRowThreads>(a, blockIdx.x, gridDim.x, &sh.share, sh.scan,
-                                          blockIdx.x == 0 ? prefix : nullptr);
-    int64_t at = sh.share.ts;
-    const int64_t te = sh.share.te;
-    int64_t slot = sh.share.slot, slot_first = sh.share.first;
+    const int n = lane >> 2, c = lane & 3;  // fragment coordinates
+    uint4 *sq = reinterpret_cast<uint4 *>(smem);
+    float *stats = reinterpret_cast<float *>(smem + C::kOffStats);  // [maximum, sum][warp][16 rows]
+    float *states = reinterpret_cast<float *>(smem + C::kOffRing);  // [warp][12 rows][kMergePitch], at an item's end
+    const uint32_t ring = smem_u32(smem + C::kOffRing) + warp * C::kRing * C::kSlot;
+    chunk_share<1, kDecKeys, kDecThreads>(a, blockIdx.x, gridDim.x, &share, scan, blockIdx.x == 0 ? prefix : nullptr);
+    int64_t at = share.ts, slot = share.slot, first = share.first;
+    const int64_t te = share.te;
     const float c2 = a.scale * 1.4426950408889634f;
-    const uint8_t *kp = static_cast<const uint8_t *>(a.pool.k), *vp = static_cast<const uint8_t *>(a.pool.v);
 
     while (at < te) {
-        ChunkGroup g = chunk_group<kTok, kKeys>(a, slot);
-        while (at >= slot_first + 2 * (int64_t)g.nt) {  // empty slots between two groups
-            slot_first += 2 * (int64_t)g.nt;
-            g = chunk_group<kTok, kKeys>(a, ++slot);
+        ChunkGroup g = chunk_group<1, kDecKeys>(a, slot);
+        while (at >= first + 2 * (int64_t)g.nt) {  // empty slots between two tokens
+            first += 2 * (int64_t)g.nt;
+            g = chunk_group<1, kDecKeys>(a, ++slot);
         }
-        const int hd = at >= slot_first + g.nt ? 1 : 0;  // KV head
-        const int64_t item_first = slot_first + (int64_t)hd * g.nt;
-        const int i0 = (int)(at - item_first);
-        const int i1 = te - item_first < g.nt ? (int)(te - item_first) : g.nt;
-        const int64_t t_first = g.t0 > 0 ? g.t0 : 0, t_last = g.t0 + g.nq - 1;
+        const int hd = at >= first + g.nt ? 1 : 0;  // KV head
+        const int64_t item = first + (int64_t)hd * g.nt;
+        const int i0 = (int)(at - item), i1 = te - item < g.nt ? (int)(te - item) : g.nt;
+        const int t = (int)g.t0, ns = g.ns, w_tile = (int)g.w_tile;
+        const int near = a.window > 0 && a.window <= t ? t - (int)a.window + 1 : 0, sinks = (int)a.sinks;
+        const int64_t row_q = g.row0 * kHQ + hd * kGrp;
+        const int32_t *table = a.pool.table + (int64_t)g.s * a.pool.max_pages;
+        auto sees = [&](int j) -> bool { return j <= t && (j >= near || j < sinks); };
+        auto tile = [&](int i) -> int { return (i < ns ? i : w_tile + (i - ns)) * kDecKeys + warp * 16; };
 
-        // the pool rows of tile i's keys: 0 .. kKeys - 1 threads, one key each
-        auto key_row = [&](int i) -> int32_t {
-            if (i >= i1) return -1;
-            const int64_t j = tile_start(g, i, kKeys) + tid;
-            const bool any = j <= t_last && (a.window <= 0 || t_first - j < a.window || j < a.sinks);
-            return any ? (int32_t)chunk_pool_row(a.pool, g.s, j) : -1;
+        // A lane looks up key lane mod 16 of the warp's 16.  The page is fetched a tile ahead of its use.
+        constexpr int32_t kUnseen = -2;
+        int32_t page = kUnseen, row = -1;
+        uint32_t off = 0u, sc[C::kAhead + 1];
+        auto fetch = [&](int i) {
+            page = kUnseen;
+            if (i >= i1) return;
+            const int j = tile(i) + (lane & 15);
+            if (!sees(j)) return;
+            const uint32_t p = a.pool.page_of((uint32_t)j, &off);
+            page = p < (uint32_t)a.pool.max_pages ? __ldg(table + p) : -1;
         };
-        __syncthreads();  // the previous item's last reads of shared memory
-        if (tid < kKeys) {
-            sh.row[0][tid] = key_row(i0);
-            sh.row[1][tid] = key_row(i0 + 1);
-            if (kFp8) {
-                const int32_t r = sh.row[0][tid];
-                sh.ks[0][tid] = r >= 0 ? scale_of_byte(__ldg(a.pool.k_scales + (int64_t)r * 2 + hd)) : 0.f;
-                sh.vs[0][tid] = r >= 0 ? scale_of_byte(__ldg(a.pool.v_scales + (int64_t)r * 2 + hd)) : 0.f;
+        auto resolve = [&]() -> uint32_t {  // -> this lane's scale: of K (lanes 0 .. 15) or V
+            row = -1;
+            if (page != kUnseen) {
+                if ((uint32_t)page < (uint32_t)a.pool.num_pages)
+                    row = (page * a.pool.page_size + (int32_t)off) * kHKV + hd;
+                else
+                    set_device_status(QSA_ERR_DEVICE_CHECK);
             }
+            if (!kFp8) return 0u;
+            return row >= 0 ? (uint32_t)__ldg((lane < 16 ? a.pool.k_scales : a.pool.v_scales) + row) : 127u;
+        };
+        uint32_t put = 0, get = 0;  // ring slots
+        auto copy = [&](const void *base, int pitch) {
+            const uint32_t dst = ring + put * C::kSlot;
+            put = put + 1 == C::kRing ? 0 : put + 1;
+#pragma unroll
+            for (int x = 0; x < (kFp8 ? 8 : 16); ++x) {
+                const int key = kFp8 ? 2 * x + (lane >> 4) : x, col = (kFp8 ? lane & 15 : lane) * 16;
+                const int32_t r = __shfl_sync(0xffffffffu, row, key);
+                const uint8_t *src = static_cast<const uint8_t *>(base) + (int64_t)(r < 0 ? 0 : r) * C::kRow + col;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                             ::"r"(dst + key * pitch + col), "l"(src), "r"(r >= 0 ? 16 : 0) : "memory");
+            }
+        };
+        auto commit = [&]() { asm volatile("cp.async.commit_group;" ::: "memory"); };
+        auto arrived = [&]() {  // the oldest half tile on its way
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::kRing - 1) : "memory");
+            __syncwarp();
+        };
+
+        // the first tiles are on their way while Q is laid out
+        fetch(i0);
+#pragma unroll
+        for (int x = 0; x < C::kAhead; ++x) {
+            sc[x] = resolve();
+            fetch(i0 + x + 1);
+            copy(a.pool.k, C::kPitchK);
+            commit();
+            copy(a.pool.v, C::kPitchV);
+            commit();
         }
-        for (int x = tid; x < kMT * 16 * 32; x += kRowThreads) {
-            const int mt = x / 512, st = (x / 32) % 16, ln = x & 31;
-            const int r0 = mt * 16 + (ln >> 2);
+        for (int x = tid; x < 16 * 32; x += kDecThreads) {
+            const int st = x >> 5, ln = x & 31, r0 = ln >> 2;
             const int d = kFp8 ? (st >> 2) * 64 + (ln & 3) * 16 + (st & 3) * 4 : (st >> 1) * 32 + (ln & 3) * 8 + (st & 1) * 4;
-            uint2 lo = make_uint2(0u, 0u), hi = lo;
-            const __nv_bfloat16 *src = a.q + (g.row0 * kHQ + hd * kGrp) * kD + d;
-            if (r0 / kGrp < g.nq)
-                lo = __ldg(reinterpret_cast<const uint2 *>(src + ((int64_t)(r0 / kGrp) * kHQ + r0 % kGrp) * kD));
-            if ((r0 + 8) / kGrp < g.nq)
-                hi = __ldg(reinterpret_cast<const uint2 *>(src + ((int64_t)((r0 + 8) / kGrp) * kHQ + (r0 + 8) % kGrp) * kD));
-            sh.q[mt][st][ln] = make_uint4(lo.x, hi.x, lo.y, hi.y);
+            const __nv_bfloat16 *src = a.q + (row_q + r0) * kD + d;
+            const uint2 lo = __ldg(reinterpret_cast<const uint2 *>(src));
+            const uint2 hi = r0 + 8 < kGrp ? __ldg(reinterpret_cast<const uint2 *>(src + 8 * kD)) : make_uint2(0u, 0u);
+            sq[x] = make_uint4(lo.x, hi.x, lo.y, hi.y);
         }
         __syncthreads();
 
-        uint4 kr[C::kNT][C::kPieces];
-        auto load_k = [&](int buf) {
+        float o[32][4];
 #pragma unroll
-            for (int nt = 0; nt < C::kNT; ++nt) {
-                const int32_t r = sh.row[buf][warp * (kKeys / kRowWarps) + nt * 8 + n];
-                const uint8_t *src = kp + ((int64_t)r * kHKV + hd) * kBytes + c * 16;
+        for (int j = 0; j < 32; ++j)
 #pragma unroll
-                for (int i = 0; i < C::kPieces; ++i)
-                    kr[nt][i] = r >= 0 ? ld_stream16(src + i * 64) : make_uint4(0u, 0u, 0u, 0u);
-            }
-        };
-        load_k(0);
+            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of rows n and n + 8
 
-        float o[kMT][4][4];
-        float m[kMT][2], l[kMT][2];
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][j][e] = 0.f;
-            m[mt][0] = m[mt][1] = -INFINITY;
-            l[mt][0] = l[mt][1] = 0.f;
-        }
-        // positions of this thread's rows; a row without a token sees no key
-        int64_t t_row[kMT][2];
-#pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = mt * 16 + n + 8 * e;
-                t_row[mt][e] = r / kGrp < g.nq ? g.t0 + r / kGrp : (int64_t)-1;
-            }
-
-        int cur = 0, nxt = 1, aft = 2;  // ring of the pool rows: this tile's, the next one's, the one after
         for (int i = i0; i < i1; ++i) {
-            const int par = (i - i0) & 1;
-            // V of this tile
-            uint32_t vr[C::kKS][4][kFp8 ? 1 : 2];
+            // K of this tile; a warp's key (x >> 1) + 4 (x & 1) + 8 y is column x of S's part y
+            sc[C::kAhead] = resolve();
+            fetch(i + C::kAhead + 1);
+            __syncwarp();  // all lanes have read the slot that is filled next
+            copy(a.pool.k, C::kPitchK);
+            commit();
+            arrived();
+            const uint32_t k_slot = ring + get * C::kSlot + c * 16 + ((n >> 1) + 4 * (n & 1)) * C::kPitchK;
+            get = get + 1 == C::kRing ? 0 : get + 1;
+            float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-            for (int ks = 0; ks < C::kKS; ++ks) {
-                const int4 r4 = *reinterpret_cast<const int4 *>(&sh.row[cur][ks * 16 + c * 4]);
-                const int32_t r[4] = {r4.x, r4.y, r4.z, r4.w};
+            for (int x = 0; x < (kFp8 ? 4 : 8); ++x) {
+                uint4 w[2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint8_t *src = vp + ((int64_t)r[e] * kHKV + hd) * kBytes + (warp * 32 + n * 4) * (kFp8 ? 1 : 2);
+                for (int y = 0; y < 2; ++y) w[y] = lds16(k_slot + y * 8 * C::kPitchK + x * 64);
+#pragma unroll
+                for (int z = 0; z < (kFp8 ? 4 : 2); ++z) {
+                    const uint4 qa = sq[(x * (kFp8 ? 4 : 2) + z) * 32 + lane];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t b0, b1;
+                        if (kFp8) {
+                            codes_to_bf16(z == 0 ? w[y].x : (z == 1 ? w[y].y : (z == 2 ? w[y].z : w[y].w)), b0, b1);
+                        } else {
+                            b0 = z == 0 ? w[y].x : w[y].z;
+                            b1 = z == 0 ? w[y].y : w[y].w;
+                        }
+                        mma_16816(s[y], qa, b0, b1);
+                    }
+                }
+            }
+            // scale, mask, row maxima: this lane's keys are c, c + 4 (part 0), c + 8, c + 12 (part 1)
+            const int j0 = tile(i);
+            const bool whole = j0 + 15 <= t && (j0 >= near || j0 + 16 <= sinks);
+            float vs[2][2], mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int key = c + 4 * x + 8 * y;
+                    float f = c2;
+                    vs[y][x] = 1.f;
                     if (kFp8) {
-                        vr[ks][e][0] = r[e] >= 0 ? __ldg(reinterpret_cast<const uint32_t *>(src)) : 0u;
-                    } else {
-                        const uint2 x = r[e] >= 0 ? __ldg(reinterpret_cast<const uint2 *>(src)) : make_uint2(0u, 0u);
-                        vr[ks][e][0] = x.x;
-                        vr[ks][e][kFp8 ? 0 : 1] = x.y;
+                        f *= scale_of_byte(__shfl_sync(0xffffffffu, sc[0], key));
+                        vs[y][x] = scale_of_byte(__shfl_sync(0xffffffffu, sc[0], key + 16));
+                    }
+                    const bool hidden = !whole && !sees(j0 + key);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float z = hidden ? -INFINITY : s[y][2 * h + x] * f;
+                        s[y][2 * h + x] = z;
+                        mx[h] = fmaxf(mx[h], z);
+                    }
+                }
+            bool grow = false;
+            float base[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+                grow |= m[h] != -INFINITY && mx[h] > m[h] + 8.f;
+            }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float to = fmaxf(m[h], mx[h]);
+                    const float f = m[h] == -INFINITY ? 1.f : dec_ex2(m[h] - to);
+                    m[h] = to;
+                    l[h] *= f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        o[j][2 * h] *= f;
+                        o[j][2 * h + 1] *= f;
                     }
                 }
             }
-            // S of this warp's keys
-            float s[C::kNT][kMT][4];
+            uint32_t pa[2][2];  // [part][row half]
 #pragma unroll
-            for (int nt = 0; nt < C::kNT; ++nt)
+            for (int h = 0; h < 2; ++h) {
+                if (m[h] == -INFINITY) m[h] = mx[h];
+                base[h] = m[h] == -INFINITY ? 0.f : m[h];  // no visible key yet
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) s[nt][mt][e] = 0.f;
-#pragma unroll
-            for (int st = 0; st < 16; ++st) {
-                uint4 qa[kMT];
-#pragma unroll
-                for (int mt = 0; mt < kMT; ++mt) qa[mt] = sh.q[mt][st][lane];
-#pragma unroll
-                for (int nt = 0; nt < C::kNT; ++nt) {
-                    uint32_t b0, b1;
-                    if (kFp8) {
-                        const uint4 &x = kr[nt][st >> 2];
-                        const uint32_t w = (st & 3) == 0 ? x.x : ((st & 3) == 1 ? x.y : ((st & 3) == 2 ? x.z : x.w));
-                        b0 = codes_to_bf16(__byte_perm(w, 0u, 0x1100));
-                        b1 = codes_to_bf16(__byte_perm(w, 0u, 0x3322));
-                    } else {
-                        const uint4 &x = kr[nt][(st >> 1) % C::kPieces];
-                        b0 = (st & 1) ? x.z : x.x;
-                        b1 = (st & 1) ? x.w : x.y;
+                for (int y = 0; y < 2; ++y) {
+                    float p0 = dec_ex2(s[y][2 * h] - base[h]), p1 = dec_ex2(s[y][2 * h + 1] - base[h]);
+                    l[h] += p0 + p1;
+                    if (kFp8) {  // a hidden key's scale may be a NaN (a row with a non-finite value): P stays 0
+                        p0 = p0 == 0.f ? 0.f : p0 * vs[y][0];
+                        p1 = p1 == 0.f ? 0.f : p1 * vs[y][1];
                     }
-#pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt) mma_16816(s[nt][mt], qa[mt], b0, b1);
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(p0, p1);
+                    pa[y][h] = *reinterpret_cast<const uint32_t *>(&p);
                 }
             }
-            // the next tile's K, its scales, and the pool rows of the tile after it
-            int32_t row2 = -1;
-            uint32_t kb = 0u, vb = 0u;
-            if (i + 1 < i1) {
-                load_k(nxt);
-                if (tid < kKeys) {
-                    row2 = key_row(i + 2);
-                    if (kFp8) {
-                        const int64_t r = sh.row[nxt][tid];
-                        kb = r >= 0 ? __ldg(a.pool.k_scales + r * 2 + hd) : 0u;
-                        vb = r >= 0 ? __ldg(a.pool.v_scales + r * 2 + hd) : 0u;
+            const uint4 pf = make_uint4(pa[0][0], pa[0][1], pa[1][0], pa[1][1]);
+            // V
+            __syncwarp();
+            copy(a.pool.v, C::kPitchV);
+            commit();
+            arrived();
+            const uint32_t v_slot = ring + get * C::kSlot;
+            get = get + 1 == C::kRing ? 0 : get + 1;
+            if (kFp8) {
+                // dims 128 x + 16 n .. + 15 of the keys c, c + 4, c + 8, c + 12: 16 column tiles
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    uint4 w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = lds16(v_slot + (c + 4 * e) * C::kPitchV + x * 128 + n * 16);
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        uint32_t k[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) k[e] = z == 0 ? w[e].x : (z == 1 ? w[e].y : (z == 2 ? w[e].z : w[e].w));
+                        uint32_t b0[4], b1[4];
+                        codes_to_bf16(__byte_perm(k[0], k[1], 0x5140), b0[0], b0[1]);
+                        codes_to_bf16(__byte_perm(k[0], k[1], 0x7362), b0[2], b0[3]);
+                        codes_to_bf16(__byte_perm(k[2], k[3], 0x5140), b1[0], b1[1]);
+                        codes_to_bf16(__byte_perm(k[2], k[3], 0x7362), b1[2], b1[3]);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) mma_16816(o[x * 16 + z * 4 + b], pf, b0[b], b1[b]);
                     }
                 }
-            }
-            // scale, mask, row maxima
-            const int64_t j0 = tile_start(g, i, kKeys);
-            // every row sees every key of the tile: no test per entry
-            const bool whole = g.t0 >= 0 && j0 + kKeys - 1 <= g.t0 && g.nq == kTok &&
-                               (a.window <= 0 || t_last - j0 < a.window || j0 + kKeys <= a.sinks);
-            float mx[kMT][2];
+            } else {
+                // matrices of 8 keys by 8 dims, transposed: rows are the keys of S's columns
+                const int kr = lane & 7, part = (lane >> 3) & 1;
+                const uint32_t src = v_slot + ((kr >> 1) + 4 * (kr & 1) + 8 * part) * C::kPitchV + (lane >> 4) * 16;
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) mx[mt][0] = mx[mt][1] = -INFINITY;
-#pragma unroll
-            for (int nt = 0; nt < C::kNT; ++nt) {
-                const int key = warp * (kKeys / kRowWarps) + nt * 8 + 2 * c;
-                const float f0 = kFp8 ? c2 * sh.ks[par][key] : c2, f1 = kFp8 ? c2 * sh.ks[par][key + 1] : c2;
-#pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = s[nt][mt][e] * ((e & 1) ? f1 : f0);
-                        if (!whole && !chunk_sees(t_row[mt][e >> 1], j0 + key + (e & 1), a.window, a.sinks)) x = -INFINITY;
-                        s[nt][mt][e] = x;
-                        mx[mt][e >> 1] = fmaxf(mx[mt][e >> 1], x);
-                    }
-            }
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x = mx[mt][e];
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                    if (c == 0) sh.wmax[warp][mt * 16 + n + 8 * e] = x;
-                }
-            __syncthreads();
-            float f[kMT][2];
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float x = m[mt][e];
-#pragma unroll
-                    for (int w = 0; w < kRowWarps; ++w) x = fmaxf(x, sh.wmax[w][mt * 16 + n + 8 * e]);
-                    const float base = x == -INFINITY ? 0.f : x;  // no visible key yet
-                    f[mt][e] = exp2f(m[mt][e] - base);
-                    m[mt][e] = x;
-                    mx[mt][e] = base;
-                    l[mt][e] *= f[mt][e];
-                }
-            // P, its row sums (of the unrounded values), and the values' scales folded in
-#pragma unroll
-            for (int nt = 0; nt < C::kNT; ++nt) {
-                const int key = warp * (kKeys / kRowWarps) + nt * 8 + 2 * c;
-                const float v0 = kFp8 ? sh.vs[par][key] : 1.f, v1 = kFp8 ? sh.vs[par][key + 1] : 1.f;
-                // key 4 x + y of a 16-key step is column 2 x + (y & 1) + 8 (y >> 1): a lane's four
-                // keys of a step are then consecutive in the cache
-                const int k16 = key & 15, col = (key & ~15) + 2 * (k16 >> 2) + ((k16 & 2) << 2);
-#pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float p0 = exp2f(s[nt][mt][2 * e] - mx[mt][e]), p1 = exp2f(s[nt][mt][2 * e + 1] - mx[mt][e]);
-                        l[mt][e] += p0 + p1;
-                        // a masked key's scale may be a NaN (a row with a non-finite value): P stays 0
-                        const float w0 = kFp8 ? (p0 == 0.f ? 0.f : p0 * v0) : p0, w1 = kFp8 ? (p1 == 0.f ? 0.f : p1 * v1) : p1;
-                        *reinterpret_cast<__nv_bfloat162 *>(&sh.p[mt * 16 + n + 8 * e][col]) = __floats2bfloat162_rn(w0, w1);
-                    }
-            }
-            if (tid < kKeys && i + 1 < i1) {
-                sh.row[aft][tid] = row2;
-                if (kFp8) {
-                    sh.ks[par ^ 1][tid] = scale_of_byte(kb);
-                    sh.vs[par ^ 1][tid] = scale_of_byte(vb);
+                for (int x = 0; x < 16; ++x) {
+                    const uint4 b = ldmatrix4t(src + x * 32);
+                    mma_16816(o[2 * x], pf, b.x, b.y);
+                    mma_16816(o[2 * x + 1], pf, b.z, b.w);
                 }
             }
-            __syncthreads();
-            // O = O f + P V
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[mt][j][e] *= f[mt][e >> 1];
-#pragma unroll
-            for (int ks = 0; ks < C::kKS; ++ks) {
-                uint4 pa[kMT];
-#pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
-                    pa[mt] = ldmatrix4(smem_u32(&sh.p[mt * 16 + (lane & 15)][ks * 16 + (lane >> 4) * 8]));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t b0, b1;
-                    if (kFp8) {
-                        const uint32_t sel = j * 0x11u | (4 + j) * 0x1100u;
-                        b0 = codes_to_bf16(__byte_perm(vr[ks][0][0], vr[ks][1][0], sel));
-                        b1 = codes_to_bf16(__byte_perm(vr[ks][2][0], vr[ks][3][0], sel));
-                    } else {
-                        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-                        const int hh = kFp8 ? 0 : j >> 1;
-                        b0 = __byte_perm(vr[ks][0][hh], vr[ks][1][hh], sel);
-                        b1 = __byte_perm(vr[ks][2][hh], vr[ks][3][hh], sel);
-                    }
-#pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt) mma_16816(o[mt][j], pa[mt], b0, b1);
-                }
-            }
-            const int t = cur;
-            cur = nxt;
-            nxt = aft;
-            aft = t;
+            for (int x = 0; x < C::kAhead; ++x) sc[x] = sc[x + 1];
         }
+        asm volatile("cp.async.wait_all;" ::: "memory");
 
-        // row sums over the warps' keys
+        // the eight warps' states, through shared memory in the place of their rings
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float x = l[mt][e];
-                x += __shfl_xor_sync(0xffffffffu, x, 1);
-                x += __shfl_xor_sync(0xffffffffu, x, 2);
-                if (c == 0) sh.wsum[warp][mt * 16 + n + 8 * e] = x;
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+            if (c == 0) {
+                stats[warp * 16 + n + 8 * h] = m[h];
+                stats[(kDecWarps + warp) * 16 + n + 8 * h] = l[h];
             }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int r = n + 8 * h;
+            if (r >= kGrp) continue;
+            float *dst = states + (warp * kGrp + r) * C::kMergePitch;
+            if (kFp8) {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const int j = x * 16 + z * 4;
+                            *reinterpret_cast<float4 *>(dst + x * 128 + (2 * c + e) * 16 + z * 4) =
+                                make_float4(o[j][2 * h + e], o[j + 1][2 * h + e], o[j + 2][2 * h + e], o[j + 3][2 * h + e]);
+                        }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    *reinterpret_cast<float2 *>(dst + 8 * j + 2 * c) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
+            }
+        }
         __syncthreads();
         const bool complete = i0 == 0 && i1 == g.nt;
         const int64_t piece = 2 * (int64_t)blockIdx.x + (i0 == 0 ? 1 : 0);
+        // a thread adds up 12 dims: four of rows tid / 64, + 4 and + 8
+        for (int r = tid >> 6; r < kGrp; r += 4) {
+            const int d = (tid & 63) * 4;
+            float top = -INFINITY;
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
+            for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, stats[w * 16 + r]);
+            const float b = top == -INFINITY ? 0.f : top;
+            float L = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = mt * 16 + n + 8 * e;
-                if (r / kGrp >= g.nq) continue;
-                float L = 0.f;
-#pragma unroll
-                for (int w = 0; w < kRowWarps; ++w) L += sh.wsum[w][r];
-                const bool none = L == 0.f;  // (a NaN is not)
-                const float inv = none ? 0.f : 1.f / L;
-                const float lse2 = none ? -INFINITY : m[mt][e] + log2f(L);
-                float x[8];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[j] = none ? 0.f : o[mt][j][2 * e] * inv;
-                    x[4 + j] = none ? 0.f : o[mt][j][2 * e + 1] * inv;
-                }
-                const int d = warp * 32 + c * 8;
-                if (complete) {
-                    const int64_t row = (g.row0 + r / kGrp) * kHQ + hd * kGrp + r % kGrp;
-                    __nv_bfloat162 h[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-                    *reinterpret_cast<uint4 *>(a.o + row * kD + d) = *reinterpret_cast<const uint4 *>(h);
-                    if (a.lse != nullptr && warp == 0 && c == 0) a.lse[row] = lse2 * 0.6931471805599453f;
-                } else {
-                    float *dst = a.ws + (piece * kRows + r) * kD + d;
-                    *reinterpret_cast<float4 *>(dst) = make_float4(x[0], x[1], x[2], x[3]);
-                    *reinterpret_cast<float4 *>(dst + 4) = make_float4(x[4], x[5], x[6], x[7]);
-                    if (warp == 0 && c == 0) a.ws[2 * (int64_t)gridDim.x * kRows * kD + piece * kRows + r] = lse2;
-                }
+            for (int w = 0; w < kDecWarps; ++w) {
+                const float f = exp2f(stats[w * 16 + r] - b);
+                const float4 x = *reinterpret_cast<const float4 *>(states + (w * kGrp + r) * C::kMergePitch + d);
+                L = fmaf(f, stats[(kDecWarps + w) * 16 + r], L);
+                acc.x = fmaf(f, x.x, acc.x);
+                acc.y = fmaf(f, x.y, acc.y);
+                acc.z = fmaf(f, x.z, acc.z);
+                acc.w = fmaf(f, x.w, acc.w);
             }
-        at = item_first + i1;
+            const bool none = L == 0.f;  // (a NaN is not)
+            const float inv = none ? 0.f : 1.f / L;
+            const float lse2 = none ? -INFINITY : top + log2f(L);
+            acc = none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+            if (complete) {
+                const __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x, acc.y), h1 = __floats2bfloat162_rn(acc.z, acc.w);
+                *reinterpret_cast<uint2 *>(a.o + (row_q + r) * kD + d) =
+                    make_uint2(*reinterpret_cast<const uint32_t *>(&h0), *reinterpret_cast<const uint32_t *>(&h1));
+                if (a.lse != nullptr && d == 0) a.lse[row_q + r] = lse2 * 0.6931471805599453f;
+            } else {
+                *reinterpret_cast<float4 *>(a.ws + (piece * kGrp + r) * kD + d) = acc;
+                if (d == 0) a.ws[2 * (int64_t)gridDim.x * kGrp * kD + piece * kGrp + r] = lse2;
+            }
+        }
+        __syncthreads();  // the next item's copies overwrite the states
+        at = item + i1;
     }
 }
 
-constexpr int64_t kMaxWorkers = 512;  // CTAs of the rows kernel, at most (the workspace's bound)
+constexpr int64_t kMaxWorkers = 160;  // CTAs of the kernel, at most (the workspace's bound)
 
-size_t rows_prefix_offset(int rows) { return (size_t)(2 * kMaxWorkers) * rows * (kD + 1) * sizeof(float); }
+size_t dec_prefix_offset() { return (size_t)(2 * kMaxWorkers) * kGrp * (kD + 1) * sizeof(float); }
 
-template <int kMT, bool kFp8>
-cudaError_t launch_rows(const ChunkArgs &a, cudaStream_t stream)
+template <bool kFp8>
+cudaError_t launch_decode(const ChunkArgs &a, cudaStream_t stream)
 {
-    constexpr int kTok = row_tokens<kMT>(), kRows = kTok * kGrp, kKeys = RowCfg<kFp8>::kKeys;
-    int64_t *prefix = reinterpret_cast<int64_t *>(reinterpret_cast<uint8_t *>(a.ws) + rows_prefix_offset(kRows));
-    int64_t workers = (int64_t)num_sms() * 2;
+    int64_t *prefix = reinterpret_cast<int64_t *>(reinterpret_cast<uint8_t *>(a.ws) + dec_prefix_offset());
+    int64_t workers = num_sms();
     if (workers > kMaxWorkers) workers = kMaxWorkers;
-    cudaError_t e = launch_pdl(chunk_rows_kernel<kMT, kFp8>, dim3((unsigned)workers), dim3(kRowThreads), 0, stream, a, prefix);
+    cudaError_t e = set_smem_attr_once(reinterpret_cast<const void *>(chunk_decode_kernel<kFp8>), DecCfg<kFp8>::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_chunk_merge<kTok, kKeys>(a, prefix, workers, stream);
+    e = launch_pdl(chunk_decode_kernel<kFp8>, dim3((unsigned)workers), dim3(kDecThreads), DecCfg<kFp8>::kSmem, stream, a,
+                   prefix);
+    if (e != cudaSuccess) return e;
+    return launch_chunk_merge<1, kDecKeys>(a, prefix, workers, stream);
 }
 
 }  // namespace
 
 size_t chunk_workspace_bytes(int batch, int64_t total_q)
 {
-    const size_t rows = row_tokens<3>() * kGrp;
-    const size_t own = rows_prefix_offset(rows) + (size_t)(chunk_slots<1>(total_q, batch) + 1) * sizeof(int64_t);
+    const size_t own = dec_prefix_offset() + (size_t)(chunk_slots<1>(total_q, batch) + 1) * sizeof(int64_t);
     const size_t tc = chunk_tc_workspace_bytes(batch, total_q);
     return own > tc ? own : tc;
 }
@@ -438,7 +436,7 @@ size_t chunk_workspace_bytes(int batch, int64_t total_q)
 cudaError_t launch_chunk_attn(const ChunkArgs &a, cudaStream_t stream)
 {
     if (a.total_q <= 0) return cudaSuccess;
-    if (a.max_len_q <= 1) return a.pool.fp8 ? launch_rows<1, true>(a, stream) : launch_rows<1, false>(a, stream);
+    if (a.max_len_q <= 1) return a.pool.fp8 ? launch_decode<true>(a, stream) : launch_decode<false>(a, stream);
     return launch_chunk_tc(a, stream);
 }
 
