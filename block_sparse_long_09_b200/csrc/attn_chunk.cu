@@ -15,11 +15,18 @@
 //     P's operand as they are; the order of the 256 dims inside S, of the dims of O and of a
 //     warp's 16 keys is free, and chosen so that a lane's loads are 16 contiguous bytes
 //     without bank conflicts (rows of the ring are padded by 16 or 32 bytes for that).
-//   * e4m3 codes become bf16 by moving their 7 low bits to the top of a bf16 and
-//     multiplying by 2^120; exact.  The keys' scales multiply S, the values' scales multiply P:
-//     powers of two, exact as well (P rounds to bf16: 2^-9 relative, as in every attention
-//     kernel of this library).
+//   * e4m3 codes become fp16, two per conversion instruction, exactly; so Q and P are fp16 too.
+//     (Made bf16 by shifts and masks the codes cost 700 integer operations per 16 keys, the bound:
+//     568 us at batch 64; as e4m3 operands of m16n8k32 against Q in three e4m3 parts 714 us.)
+//     Q is scaled by a power of two per row, its largest value into [2^14, 2^15): exact for
+//     values down to 2^-31 of the row's largest, off by 2^-39 of it below.
+//     The keys' scales multiply S.  The values' scales multiply P, p 2^e, which is held relative
+//     to the row's largest so far (a power of two, as the running maximum): 2^-12 relative,
+//     or below 2^-18 of the largest an absolute 2^-29 of it.
+//   * bf16 pools: P rounds to bf16, 2^-8 relative at most, as in every attention kernel here.
 //   * O is rescaled only when a row's maximum grows by more than 2^8.
+#include <cuda_fp16.h>
+
 #include "chunk_common.cuh"
 
 namespace qsa {
@@ -38,13 +45,22 @@ struct DecCfg {
     static constexpr int kOffRing = 16 * 32 * 16;                    // behind Q's fragments
     static constexpr int kMergePitch = kD + 4;                       // floats per row of a warp's state
     static constexpr int kOffStats = kOffRing + kDecWarps * kRing * kSlot;
-    static constexpr int kSmem = kOffStats + 2 * kDecWarps * 16 * (int)sizeof(float);
+    static constexpr int kOffScale = kOffStats + 2 * kDecWarps * 16 * (int)sizeof(float);
+    static constexpr int kSmem = kOffScale + 16 * (int)sizeof(float);
     static_assert(kDecWarps * kGrp * kMergePitch * 4 <= kDecWarps * kRing * kSlot, "the merge reuses the ring");
     static_assert(kSmem <= 232448 - 1024, "shared memory of one CTA");
 };
 
+template <bool kHalf>
 __device__ __forceinline__ void mma_16816(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1)
 {
+    if (kHalf)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
+            " {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+    else
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9},"
         " {%0, %1, %2, %3};"
@@ -68,17 +84,24 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr)
     return r;
 }
 
-// four codes -> the bf16 pairs of codes (0, 1) and (2, 3)
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, uint32_t &p01, uint32_t &p23)
+// four e4m3 codes -> the fp16 pairs of codes (0, 1) and (2, 3)
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t &p01, uint32_t &p23)
 {
-    const uint32_t hi = (w & 0x80808080u) | ((w >> 4) & 0x07070707u), lo = (w << 4) & 0xF0F0F0F0u;
-    const __nv_bfloat162 up = __halves2bfloat162(__ushort_as_bfloat16(0x7B80), __ushort_as_bfloat16(0x7B80));  // 2^120
-    const uint32_t a = __byte_perm(lo, hi, 0x5140), b = __byte_perm(lo, hi, 0x7362);
-    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a), up);
-    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&b), up);
-    p01 = *reinterpret_cast<const uint32_t *>(&x);
-    p23 = *reinterpret_cast<const uint32_t *>(&y);
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(p01), "=r"(p23) : "r"(w));
 }
+
+__device__ __forceinline__ uint32_t half2(float x, float y)
+{
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
 __device__ __forceinline__ float dec_ex2(float x)
 {
@@ -176,15 +199,50 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
             copy(a.pool.v, C::kPitchV);
             commit();
         }
+        // Q's fragments in the order of K's dims; e4m3: as fp16, scaled per row
+        if (kFp8) {
+            float *qs = reinterpret_cast<float *>(smem + C::kOffScale);
+            for (int r = warp; r < 16; r += kDecWarps) {
+                float top = 0.f;
+                if (r < kGrp) {
+                    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(a.q + (row_q + r) * kD + lane * 8));
+                    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u))));
+                }
+#pragma unroll
+                for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+                // the largest times 2^(14 - E) lies in [2^14, 2^15); an infinity stays one
+                const int E = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127);
+                if (lane == 0) qs[r] = pow2(E - 14);
+            }
+            __syncthreads();
+        }
         for (int x = tid; x < 16 * 32; x += kDecThreads) {
             const int st = x >> 5, ln = x & 31, r0 = ln >> 2;
             const int d = kFp8 ? (st >> 2) * 64 + (ln & 3) * 16 + (st & 3) * 4 : (st >> 1) * 32 + (ln & 3) * 8 + (st & 1) * 4;
             const __nv_bfloat16 *src = a.q + (row_q + r0) * kD + d;
-            const uint2 lo = __ldg(reinterpret_cast<const uint2 *>(src));
-            const uint2 hi = r0 + 8 < kGrp ? __ldg(reinterpret_cast<const uint2 *>(src + 8 * kD)) : make_uint2(0u, 0u);
+            uint2 lo = __ldg(reinterpret_cast<const uint2 *>(src));
+            uint2 hi = r0 + 8 < kGrp ? __ldg(reinterpret_cast<const uint2 *>(src + 8 * kD)) : make_uint2(0u, 0u);
+            if (kFp8) {
+                const float *qs = reinterpret_cast<const float *>(smem + C::kOffScale);
+                auto halves = [](uint32_t v, float up) -> uint32_t {
+                    return half2(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xFFFF0000u) * up);
+                };
+                const float u0 = 1.f / qs[r0], u1 = 1.f / qs[r0 + 8];  // (powers of two)
+                lo = make_uint2(halves(lo.x, u0), halves(lo.y, u0));
+                hi = make_uint2(halves(hi.x, u1), halves(hi.y, u1));
+            }
             sq[x] = make_uint4(lo.x, hi.x, lo.y, hi.y);
         }
         __syncthreads();
+
+        float q_down[2] = {1.f, 1.f};
+        if (kFp8) {
+            q_down[0] = reinterpret_cast<const float *>(smem + C::kOffScale)[n];
+            q_down[1] = reinterpret_cast<const float *>(smem + C::kOffScale)[n + 8];
+        }
 
         float o[32][4];
 #pragma unroll
@@ -192,6 +250,7 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
         float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // of rows n and n + 8
+        float up[2] = {INFINITY, INFINITY};                      // e4m3: O is held times this (infinity: still 0)
 
         for (int i = i0; i < i1; ++i) {
             // K of this tile; a warp's key (x >> 1) + 4 (x & 1) + 8 y is column x of S's part y
@@ -203,7 +262,7 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
             arrived();
             const uint32_t k_slot = ring + get * C::kSlot + c * 16 + ((n >> 1) + 4 * (n & 1)) * C::kPitchK;
             get = get + 1 == C::kRing ? 0 : get + 1;
-            float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, s2[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
             for (int x = 0; x < (kFp8 ? 4 : 8); ++x) {
                 uint4 w[2];
@@ -216,15 +275,20 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
                     for (int y = 0; y < 2; ++y) {
                         uint32_t b0, b1;
                         if (kFp8) {
-                            codes_to_bf16(z == 0 ? w[y].x : (z == 1 ? w[y].y : (z == 2 ? w[y].z : w[y].w)), b0, b1);
+                            codes_to_half(z == 0 ? w[y].x : (z == 1 ? w[y].y : (z == 2 ? w[y].z : w[y].w)), b0, b1);
                         } else {
                             b0 = z == 0 ? w[y].x : w[y].z;
                             b1 = z == 0 ? w[y].y : w[y].w;
                         }
-                        mma_16816(s[y], qa, b0, b1);
+                        // even and odd steps apart: shorter chains of dependent products
+                        mma_16816<kFp8>((z & 1) ? s2[y] : s[y], qa, b0, b1);
                     }
                 }
             }
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[y][e] = (s[y][e] + s2[y][e]) * (kFp8 ? q_down[e >> 1] : 1.f);
             // scale, mask, row maxima: this lane's keys are c, c + 4 (part 0), c + 8, c + 12 (part 1)
             const int j0 = tile(i);
             const bool whole = j0 + 15 <= t && (j0 >= near || j0 + 16 <= sinks);
@@ -270,23 +334,55 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
                     }
                 }
             }
-            uint32_t pa[2][2];  // [part][row half]
+            float p[2][2][2], px[2] = {0.f, 0.f};  // [row half][part][key], a row's largest
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (m[h] == -INFINITY) m[h] = mx[h];
                 base[h] = m[h] == -INFINITY ? 0.f : m[h];  // no visible key yet
 #pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    float p0 = dec_ex2(s[y][2 * h] - base[h]), p1 = dec_ex2(s[y][2 * h + 1] - base[h]);
-                    l[h] += p0 + p1;
-                    if (kFp8) {  // a hidden key's scale may be a NaN (a row with a non-finite value): P stays 0
-                        p0 = p0 == 0.f ? 0.f : p0 * vs[y][0];
-                        p1 = p1 == 0.f ? 0.f : p1 * vs[y][1];
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float e = dec_ex2(s[y][2 * h + x] - base[h]);
+                        l[h] += e;
+                        // a hidden key's scale may be a NaN (a row with a non-finite value): P stays 0
+                        p[h][y][x] = kFp8 ? (e == 0.f ? 0.f : e * vs[y][x]) : e;
+                        px[h] = fmaxf(px[h], p[h][y][x]);
                     }
-                    const __nv_bfloat162 p = __floats2bfloat162_rn(p0, p1);
-                    pa[y][h] = *reinterpret_cast<const uint32_t *>(&p);
+            }
+            if (kFp8) {
+                // p 2^e relative to 2^-up of its row: at most 2^15, at 2^4 when the reference is set
+                if (__any_sync(0xffffffffu, px[0] * up[0] > 32768.f || px[1] * up[1] > 32768.f)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        px[h] = fmaxf(px[h], __shfl_xor_sync(0xffffffffu, px[h], 1));
+                        px[h] = fmaxf(px[h], __shfl_xor_sync(0xffffffffu, px[h], 2));
+                        if (px[h] * up[h] > 32768.f) {
+                            const float to = pow2(min(max(131 - (int)(__float_as_uint(px[h]) >> 23), -110), 110));
+                            const float f = up[h] == INFINITY ? 0.f : to / up[h];  // (powers of two)
+                            up[h] = to;
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                o[j][2 * h] *= f;
+                                o[j][2 * h + 1] *= f;
+                            }
+                        }
+                    }
                 }
             }
+            uint32_t pa[2][2];  // [part][row half]
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    if (kFp8) {
+                        const float u = up[h] == INFINITY ? 0.f : up[h];
+                        pa[y][h] = half2(p[h][y][0] * u, p[h][y][1] * u);
+                    } else {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(p[h][y][0], p[h][y][1]);
+                        pa[y][h] = *reinterpret_cast<const uint32_t *>(&b);
+                    }
+                }
             const uint4 pf = make_uint4(pa[0][0], pa[0][1], pa[1][0], pa[1][1]);
             // V
             __syncwarp();
@@ -308,12 +404,12 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) k[e] = z == 0 ? w[e].x : (z == 1 ? w[e].y : (z == 2 ? w[e].z : w[e].w));
                         uint32_t b0[4], b1[4];
-                        codes_to_bf16(__byte_perm(k[0], k[1], 0x5140), b0[0], b0[1]);
-                        codes_to_bf16(__byte_perm(k[0], k[1], 0x7362), b0[2], b0[3]);
-                        codes_to_bf16(__byte_perm(k[2], k[3], 0x5140), b1[0], b1[1]);
-                        codes_to_bf16(__byte_perm(k[2], k[3], 0x7362), b1[2], b1[3]);
+                        codes_to_half(__byte_perm(k[0], k[1], 0x5140), b0[0], b0[1]);
+                        codes_to_half(__byte_perm(k[0], k[1], 0x7362), b0[2], b0[3]);
+                        codes_to_half(__byte_perm(k[2], k[3], 0x5140), b1[0], b1[1]);
+                        codes_to_half(__byte_perm(k[2], k[3], 0x7362), b1[2], b1[3]);
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) mma_16816(o[x * 16 + z * 4 + b], pf, b0[b], b1[b]);
+                        for (int b = 0; b < 4; ++b) mma_16816<kFp8>(o[x * 16 + z * 4 + b], pf, b0[b], b1[b]);
                     }
                 }
             } else {
@@ -323,8 +419,8 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
                     const uint4 b = ldmatrix4t(src + x * 32);
-                    mma_16816(o[2 * x], pf, b.x, b.y);
-                    mma_16816(o[2 * x + 1], pf, b.z, b.w);
+                    mma_16816<kFp8>(o[2 * x], pf, b.x, b.y);
+                    mma_16816<kFp8>(o[2 * x + 1], pf, b.z, b.w);
                 }
             }
 #pragma unroll
@@ -337,6 +433,14 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
         for (int h = 0; h < 2; ++h) {
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
             l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+            if (kFp8) {
+                const float down = up[h] == INFINITY ? 1.f : 1.f / up[h];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    o[j][2 * h] *= down;
+                    o[j][2 * h + 1] *= down;
+                }
+            }
             if (c == 0) {
                 stats[warp * 16 + n + 8 * h] = m[h];
                 stats[(kDecWarps + warp) * 16 + n + 8 * h] = l[h];
