@@ -43,7 +43,7 @@ struct DecCfg {
     static constexpr int kAhead = kFp8 ? 2 : 1;                      // tiles on their way beside the current one
     static constexpr int kRing = 2 * kAhead + 1;
     static constexpr int kOffRing = 16 * 32 * 16;                    // behind Q's fragments
-    static constexpr int kMergePitch = kD + 4;                       // floats per row of a warp's state
+    static constexpr int kMergePitch = kD + 16;                      // floats per row of a warp's state
     static constexpr int kOffStats = kOffRing + kDecWarps * kRing * kSlot;
     static constexpr int kOffScale = kOffStats + 2 * kDecWarps * 16 * (int)sizeof(float);
     static constexpr int kSmem = kOffScale + 16 * (int)sizeof(float);
@@ -292,26 +292,30 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
             // scale, mask, row maxima: this lane's keys are c, c + 4 (part 0), c + 8, c + 12 (part 1)
             const int j0 = tile(i);
             const bool whole = j0 + 15 <= t && (j0 >= near || j0 + 16 <= sinks);
-            float vs[2][2], mx[2] = {-INFINITY, -INFINITY};
+            float vs[2][2], mx[2];
+            const float own = kFp8 ? scale_of_byte(sc[0]) : 1.f;  // of key lane mod 16: K's, from lane 16 on V's
 #pragma unroll
             for (int y = 0; y < 2; ++y)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    const int key = c + 4 * x + 8 * y;
                     float f = c2;
-                    vs[y][x] = 1.f;
                     if (kFp8) {
-                        f *= scale_of_byte(__shfl_sync(0xffffffffu, sc[0], key));
-                        vs[y][x] = scale_of_byte(__shfl_sync(0xffffffffu, sc[0], key + 16));
+                        f *= __shfl_sync(0xffffffffu, own, c + 4 * x + 8 * y);
+                        vs[y][x] = __shfl_sync(0xffffffffu, own, c + 4 * x + 8 * y + 16);
                     }
-                    const bool hidden = !whole && !sees(j0 + key);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float z = hidden ? -INFINITY : s[y][2 * h + x] * f;
-                        s[y][2 * h + x] = z;
-                        mx[h] = fmaxf(mx[h], z);
-                    }
+                    for (int h = 0; h < 2; ++h) s[y][2 * h + x] *= f;
                 }
+            if (!whole) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        if (!sees(j0 + c + 4 * x + 8 * y)) s[y][x] = s[y][2 + x] = -INFINITY;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                mx[h] = fmaxf(fmaxf(s[0][2 * h], s[0][2 * h + 1]), fmaxf(s[1][2 * h], s[1][2 * h + 1]));
             bool grow = false;
             float base[2];
 #pragma unroll
@@ -460,7 +464,7 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
 #pragma unroll
                         for (int z = 0; z < 4; ++z) {
                             const int j = x * 16 + z * 4;
-                            *reinterpret_cast<float4 *>(dst + x * 128 + (2 * c + e) * 16 + z * 4) =
+                            *reinterpret_cast<float4 *>(dst + x * 128 + (2 * c + e) * 16 + ((z + c) & 3) * 4) =  // (no bank conflicts)
                                 make_float4(o[j][2 * h + e], o[j + 1][2 * h + e], o[j + 2][2 * h + e], o[j + 3][2 * h + e]);
                         }
             } else {
@@ -474,7 +478,7 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
         const int64_t piece = 2 * (int64_t)blockIdx.x + (i0 == 0 ? 1 : 0);
         // a thread adds up 12 dims: four of rows tid / 64, + 4 and + 8
         for (int r = tid >> 6; r < kGrp; r += 4) {
-            const int d = (tid & 63) * 4;
+            const int d = (tid & 63) * 4, at_d = kFp8 ? (d & ~15) + (((d >> 2) + (d >> 5)) & 3) * 4 : d;
             float top = -INFINITY;
 #pragma unroll
             for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, stats[w * 16 + r]);
@@ -484,7 +488,7 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
 #pragma unroll
             for (int w = 0; w < kDecWarps; ++w) {
                 const float f = exp2f(stats[w * 16 + r] - b);
-                const float4 x = *reinterpret_cast<const float4 *>(states + (w * kGrp + r) * C::kMergePitch + d);
+                const float4 x = *reinterpret_cast<const float4 *>(states + (w * kGrp + r) * C::kMergePitch + at_d);
                 L = fmaf(f, stats[(kDecWarps + w) * 16 + r], L);
                 acc.x = fmaf(f, x.x, acc.x);
                 acc.y = fmaf(f, x.y, acc.y);

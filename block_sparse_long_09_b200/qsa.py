@@ -1,7 +1,7 @@
 """Python binding of libqsa.so (the C ABI declared in include/qsa.h).
 
-Argument marshalling only: every step of the QSA path runs in the library's
-CUDA kernels.  torch supplies device memory and the current stream.  If the
+Argument marshalling only (the paged-cache calls' in csrc/binding.cpp, for its speed):
+every step of the QSA path runs in the library's CUDA kernels.  torch supplies device memory and the current stream.  If the
 shared library is missing this module raises at import time -- there is no
 fallback implementation.
 """
@@ -127,6 +127,26 @@ def default_config(**overrides) -> Config:
     for k, v in overrides.items():
         setattr(c, k, v)
     return c
+
+
+_DEFAULT_CFG = default_config()  # never handed out
+_DEFAULT_ADDR = ctypes.addressof(_DEFAULT_CFG)
+
+
+def _bind():
+    """The compiled argument checks of the paged-cache calls, which call the library loaded here."""
+    try:
+        from . import _binding as b
+    except ImportError as e:
+        raise ImportError("_binding.so is missing or does not load; build it with "
+                          "'python -m block_sparse_long_09_b200.build'") from e
+    b.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in
+             ("qsa_cache_write_paged", "qsa_cache_read_paged", "qsa_chunk_attn_paged", "qsa_rope_axes",
+              "qsa_workspace_size")))
+    return b
+
+
+_binding = _bind()
 
 
 def _check(status: int, where: str):
@@ -465,50 +485,8 @@ def dense_attn_prefill(q, k, v, cu_seqlens_q, cu_seqlens_k, max_len_q: int, o=No
     return (o, lse) if want_lse or lse is not None else o
 
 
-def _check_rows(name, t, heads: int, rows: Optional[int] = None):
-    """Packed rows must be bf16 [rows, heads, head_dim]: the kernels cannot see the extent."""
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != 256 or \
-            not t.is_contiguous() or (rows is not None and t.shape[0] != rows):
-        raise ValueError("%s must be contiguous bf16 [%s, %d, 256], got %s %s"
-                         % (name, "rows" if rows is None else rows, heads, t.dtype, tuple(t.shape)))
-
-
-def _check_i32(name, t, shape):
-    """An int32 argument of the given shape (None: any extent), contiguous."""
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape) or \
-            any(want is not None and got != want for got, want in zip(t.shape, shape)):
-        raise ValueError("expected contiguous int32 %s for %s, got %s %s" % (shape, name, t.dtype, tuple(t.shape)))
-
-
-def _same_device(first, *rest):
-    """Every tensor of a call lies on one device, and it is the current one (calls launch on
-    the current device's stream)."""
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError("tensors on %s and %s in one call" % (first.device, t.device))
-    if first.is_cuda and first.device.index != torch.cuda.current_device():
-        raise ValueError("tensors on %s, but the current device is cuda:%d" % (first.device, torch.cuda.current_device()))
-
-
-def _pool(k_pages, v_pages, k_scales, v_scales, block_table, batch: int):
-    """The format of a paged K/V pool, after checking its tensors: bf16, or float8_e4m3fn with
-    one uint8 scale (a biased power-of-two exponent) per (token, KV head)."""
-    if k_pages.dtype not in (torch.bfloat16, torch.float8_e4m3fn) or v_pages.dtype != k_pages.dtype:
-        raise ValueError("pages must be bfloat16 or float8_e4m3fn, both alike, got %s and %s"
-                         % (k_pages.dtype, v_pages.dtype))
-    if k_pages.dim() != 4 or tuple(k_pages.shape[2:]) != (2, 256) or v_pages.shape != k_pages.shape or \
-            not k_pages.is_contiguous() or not v_pages.is_contiguous():
-        raise ValueError("pages must be contiguous [num_pages, page_size, 2, 256], got %s and %s"
-                         % (tuple(k_pages.shape), tuple(v_pages.shape)))
-    _check_i32("block_table", block_table, (batch, None))
-    fp8 = k_pages.dtype == torch.float8_e4m3fn
-    if fp8:
-        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-            if t is None or t.dtype != torch.uint8 or t.shape != k_pages.shape[:3] or not t.is_contiguous():
-                raise ValueError("%s must be contiguous uint8 [num_pages, page_size, 2] for float8_e4m3fn pages" % name)
-    elif k_scales is not None or v_scales is not None:
-        raise ValueError("bfloat16 pages have no scales")
-    return QSA_CACHE_E4M3 if fp8 else QSA_CACHE_BF16
+def _cfg_addr(cfg: Optional[Config]) -> int:
+    return _DEFAULT_ADDR if cfg is None else ctypes.addressof(cfg)
 
 
 def cache_write_paged(k, v, k_pages, v_pages, block_table, cu_seqlens_q, cu_seqlens_k, k_scales=None, v_scales=None,
@@ -517,44 +495,20 @@ def cache_write_paged(k, v, k_pages, v_pages, block_table, cu_seqlens_q, cu_seql
     2, 256], as bf16 or, for float8_e4m3fn pages, as codes with one power-of-two scale byte per
     (token, head) in k_scales, v_scales [num_pages, page_size, 2] uint8.  Token i of
     sequence s goes to position L_k - L_q + i (cu_seqlens_k counts the new tokens)."""
-    cfg = _cfg(cfg)
-    batch = cu_seqlens_q.numel() - 1
-    fmt = _pool(k_pages, v_pages, k_scales, v_scales, block_table, batch)
-    _check_rows("k", k, cfg.n_heads_kv)
-    _check_rows("v", v, cfg.n_heads_kv, k.shape[0])
-    _check_i32("cu_seqlens_q", cu_seqlens_q, (batch + 1,))
-    _check_i32("cu_seqlens_k", cu_seqlens_k, (batch + 1,))
-    _same_device(k, v, k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens_q, cu_seqlens_k)
-    _check(_lib.qsa_cache_write_paged(ctypes.byref(cfg), _p(k), _p(v), _p(cu_seqlens_q), _p(cu_seqlens_k), batch,
-                                      k.shape[0], fmt, _p(k_pages), _p(v_pages), _p(k_scales), _p(v_scales),
-                                      k_pages.shape[0], k_pages.shape[1], _p(block_table), block_table.shape[1],
-                                      _stream()),
-           "qsa_cache_write_paged")
+    st = _binding.cache_write_paged(_cfg_addr(cfg), k, v, k_pages, v_pages, block_table, k_scales, v_scales,
+                                    cu_seqlens_q, cu_seqlens_k)
+    if st != QSA_OK:
+        raise QSAError(st, "qsa_cache_write_paged")
 
 
 def cache_read_paged(k_pages, v_pages, block_table, cu_seqlens_k, cu_out, total_out: int, tok_begin=None,
                      k_scales=None, v_scales=None, k=None, v=None, cfg: Optional[Config] = None):
     """A range of cached tokens of every sequence as packed bf16 rows k, v [total_out, 2, 256]:
     row i of sequence s (cu_out packs them) is its token tok_begin[s] + i."""
-    cfg = _cfg(cfg)
-    batch = cu_seqlens_k.numel() - 1
-    fmt = _pool(k_pages, v_pages, k_scales, v_scales, block_table, batch)
-    _check_i32("cu_seqlens_k", cu_seqlens_k, (batch + 1,))
-    _check_i32("cu_out", cu_out, (batch + 1,))
-    if tok_begin is not None:
-        _check_i32("tok_begin", tok_begin, (batch,))
-    if k is None:
-        k = torch.empty((total_out, cfg.n_heads_kv, cfg.head_dim), dtype=torch.bfloat16, device=k_pages.device)
-    if v is None:
-        v = torch.empty((total_out, cfg.n_heads_kv, cfg.head_dim), dtype=torch.bfloat16, device=k_pages.device)
-    _check_rows("k", k, cfg.n_heads_kv, total_out)
-    _check_rows("v", v, cfg.n_heads_kv, total_out)
-    _same_device(k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens_k, cu_out, tok_begin, k, v)
-    _check(_lib.qsa_cache_read_paged(ctypes.byref(cfg), fmt, _p(k_pages), _p(v_pages), _p(k_scales), _p(v_scales),
-                                     k_pages.shape[0], k_pages.shape[1], _p(block_table), block_table.shape[1],
-                                     _p(cu_seqlens_k), _p(tok_begin), _p(cu_out), batch, total_out, _p(k), _p(v),
-                                     _stream()),
-           "qsa_cache_read_paged")
+    st, k, v = _binding.cache_read_paged(_cfg_addr(cfg), k_pages, v_pages, block_table, k_scales, v_scales,
+                                         cu_seqlens_k, cu_out, total_out, tok_begin, k, v)
+    if st != QSA_OK:
+        raise QSAError(st, "qsa_cache_read_paged")
     return k, v
 
 
@@ -565,30 +519,12 @@ def chunk_attn_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, cu_seqlens_
     per sequence) over its paged bf16 or e4m3 cache, which holds them already.  window > 0: a
     token sees the last `window` positions, itself included, and the first `sinks`
     ones.  max_len_q bounds every sequence's new tokens, max_len_k (unused so far) its cache."""
-    cfg = _cfg(cfg)
-    batch = cu_seqlens_q.numel() - 1
-    fmt = _pool(k_pages, v_pages, k_scales, v_scales, block_table, batch)
-    total_q = q.shape[0]
-    _check_rows("q", q, cfg.n_heads_q)
-    _check_i32("cu_seqlens_q", cu_seqlens_q, (batch + 1,))
-    _check_i32("cu_seqlens_k", cu_seqlens_k, (batch + 1,))
-    if o is None:
-        o = torch.empty_like(q)
-    if lse is None and want_lse:
-        lse = torch.empty((total_q, cfg.n_heads_q), dtype=torch.float32, device=q.device)
-    _check_rows("o", o, cfg.n_heads_q, total_q)
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (total_q, cfg.n_heads_q)):
-        raise ValueError("lse must be fp32 [%d, %d]" % (total_q, cfg.n_heads_q))
-    if ws is None:
-        ws = torch.empty((workspace_size(OP_CHUNK_PAGED, batch, total_q, max_len_k, cfg),), dtype=torch.uint8,
-                         device=q.device)
-    _same_device(q, k_pages, v_pages, k_scales, v_scales, block_table, cu_seqlens_q, cu_seqlens_k, o, lse, ws)
-    _check(_lib.qsa_chunk_attn_paged(ctypes.byref(cfg), _p(q), fmt, _p(k_pages), _p(v_pages), _p(k_scales),
-                                     _p(v_scales), k_pages.shape[0], k_pages.shape[1], _p(block_table),
-                                     block_table.shape[1], _p(cu_seqlens_q), _p(cu_seqlens_k), batch, total_q,
-                                     max_len_q, window, sinks, _p(o), _p(lse), _p(ws), ws.numel(), _stream()),
-           "qsa_chunk_attn_paged")
-    return (o, lse) if want_lse or lse is not None else o
+    st, o, lse = _binding.chunk_attn_paged(_cfg_addr(cfg), q, k_pages, v_pages, block_table, k_scales, v_scales,
+                                           cu_seqlens_q, cu_seqlens_k, max_len_q, max_len_k, window, sinks, o, lse,
+                                           want_lse, ws)
+    if st != QSA_OK:
+        raise QSAError(st, "qsa_chunk_attn_paged")
+    return (o, lse) if lse is not None else o
 
 
 def rope_axes(q, k, positions, sections, interleaved: bool = False, inverse: bool = False, q_out=None, k_out=None,
@@ -597,31 +533,11 @@ def rope_axes(q, k, positions, sections, interleaved: bool = False, inverse: boo
     be None): positions [3, total] int32 (time, height, width), sections the pairs of each axis,
     base cfg.rope_base.  inverse=True rotates back: given the gradients of the
     outputs it returns those of the inputs.  q_out=q, k_out=k rotates in place."""
-    cfg = _cfg(cfg)
-    x = q if q is not None else k
-    if x is None:
-        raise ValueError("q or k is needed")
-    total = x.shape[0]
-    _check_i32("positions", positions, (3, total))
-    if len(sections) != 3:
-        raise ValueError("sections must be three counts of pairs")
-    for name, t, heads in (("q", q, cfg.n_heads_q), ("k", k, cfg.n_heads_kv)):
-        if t is not None:
-            _check_rows(name, t, heads, total)
-    if q is not None and q_out is None:
-        q_out = torch.empty_like(q)
-    if k is not None and k_out is None:
-        k_out = torch.empty_like(k)
-    for name, t, src, heads in (("q_out", q_out, q, cfg.n_heads_q), ("k_out", k_out, k, cfg.n_heads_kv)):
-        if t is not None:
-            if src is None:
-                raise ValueError("%s without its input" % name)
-            _check_rows(name, t, heads, total)
-    _same_device(x, q, k, positions, q_out, k_out)
+    s0, s1, s2 = sections
     flags = (QSA_ROPE_INTERLEAVED if interleaved else 0) | (QSA_ROPE_INVERSE if inverse else 0)
-    _check(_lib.qsa_rope_axes(ctypes.byref(cfg), _p(q), _p(k), _p(positions), total, int(sections[0]),
-                              int(sections[1]), int(sections[2]), flags, _p(q_out), _p(k_out), _stream()),
-           "qsa_rope_axes")
+    st, q_out, k_out = _binding.rope_axes(_cfg_addr(cfg), q, k, positions, s0, s1, s2, flags, q_out, k_out)
+    if st != QSA_OK:
+        raise QSAError(st, "qsa_rope_axes")
     return q_out, k_out
 
 
