@@ -36,10 +36,11 @@ def rotate64(x, pos, s, mixed, base, inverse=False):
         c, n = a.cos()[:, None], a.sin()[:, None]
         y[..., i], y[..., i + h] = x[..., i] * c - x[..., i + h] * n, x[..., i] * n + x[..., i + h] * c
         # sine and cosine rounded to fp32 (U32 each), two products and a sum (U32 each): 4 U32 of
-        # both magnitudes covers them; the frequency 2^-x, x <= log2(base), after three roundings
-        # of x, and the angle's own roundings; then one rounding to bf16
+        # both magnitudes covers them.  The angle in fp64, in units of 2^-53 of itself: the exponent
+        # x <= log2(base) rounds three times here and once in the formula above (x ln 2 each), the
+        # power, 1 / pi, and the products to the angle are 8 at most.  Then one rounding to bf16
         mag = x[..., i].abs() + x[..., i + h].abs()
-        e = mag * (4 * U32 + a.abs()[:, None] * (3 * math.log2(base) * math.log(2) + 4) * 2.0 ** -53)
+        e = mag * (4 * U32 + a.abs()[:, None] * (4 * math.log2(base) * math.log(2) + 8) * 2.0 ** -53)
         b[..., i], b[..., i + h] = y[..., i].abs() * U16 + e, y[..., i + h].abs() * U16 + e
     return y, b
 
