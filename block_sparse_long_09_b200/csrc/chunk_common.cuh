@@ -165,103 +165,120 @@ __device__ __forceinline__ int64_t chunk_pool_row(const CachePool &c, int64_t s,
 }
 
 constexpr int kMergeWarps = 8, kMergeThreads = kMergeWarps * 32;
+static_assert(kMergeThreads == kD, "a thread per dim");
 
-// Merge of the pieces of the cut items, and the rows of items without any visible key.  A CTA
-// per (item, row block): kSplit warps share a row's pieces (few rows: many pieces each),
-// 8 / kSplit rows at a time.
-template <int kTok, int kKeys, int kSplit>
+// Merge of the pieces of the cut items, and the rows of items without any visible key.  For few
+// rows: a CTA per row, its eight warps over the row's pieces.  Where the item's tiles lie is worked out
+// from the lengths while the attention kernel still runs (that one was scheduled after everything
+// before it had completed); only then the CTA waits for it.
+template <int kTok, int kKeys>
 __global__ void __launch_bounds__(kMergeThreads)
-chunk_merge_kernel(const ChunkArgs a, const int64_t *__restrict__ prefix, int64_t workers)
+chunk_merge_kernel(const ChunkArgs a, int64_t workers)
 {
-    constexpr int kRows = kTok * kGrp, kAt = kMergeWarps / kSplit;
-    __shared__ float part[kSplit > 1 ? kMergeWarps : 1][kD + 2];
-    pdl_enter();
-    const int64_t slot = blockIdx.x >> 1;
-    const int hd = blockIdx.x & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t slots = chunk_slots<kTok>(a.total_q, a.batch);
-    const int64_t total = prefix[slots], p0 = prefix[slot], p1 = prefix[slot + 1];
-    const int64_t nt = (p1 - p0) >> 1, rs = p0 + hd * nt, re = rs + nt;
-    int64_t c0 = 0;
-    if (nt > 0) {
-        c0 = ((rs + 1) * workers - 1) / total;  // the share that holds the item's first tile
-        if (share_start(c0 + 1, total, workers) >= re) return;  // finished by one worker
+    constexpr int kRows = kTok * kGrp, kAhead = 4;
+    __shared__ float part[kMergeWarps][kD + 2];
+    __shared__ int64_t sums[2][kMergeWarps];
+    const int slot = blockIdx.x >> 1, slots = (int)chunk_slots<kTok>(a.total_q, a.batch);
+    const int hd = blockIdx.x & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y;
+    int64_t before = 0, all = 0;
+    for (int u = threadIdx.x; u < slots; u += kMergeThreads) {
+        const int64_t n = 2 * (int64_t)chunk_group<kTok, kKeys>(a, u).nt;
+        all += n;
+        if (u < slot) before += n;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, off);
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+    }
+    if (lane == 0) {
+        sums[0][warp] = all;
+        sums[1][warp] = before;
     }
     const ChunkGroup g = chunk_group<kTok, kKeys>(a, slot);
-    const int rows = g.nq * kGrp;
+    __syncthreads();
+    int64_t total = 0, p0 = 0;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+        total += sums[0][w];
+        p0 += sums[1][w];
+    }
+    const int64_t rs = p0 + hd * (int64_t)g.nt, re = rs + g.nt;
+    int64_t c0 = 0, last = -1;
+    bool mine = r < g.nq * kGrp;
+    if (g.nt > 0) {
+        c0 = ((rs + 1) * workers - 1) / total;                                // the share that holds the item's first tile
+        if (share_start(c0 + 1, total, workers) >= re) mine = false;          // finished by one worker
+        last = (re * workers - 1) / total;                                    // and its last one
+    }
+    pdl_enter();
+    if (!mine) return;  // uniform for the CTA
     const float *lse = a.ws + 2 * workers * kRows * kD;
+    float mx = -INFINITY, sum = 0.f, acc[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] = 0.f;
     // pieces: slot 2 c0 + 1, then slot 2 c of every share c > c0 that holds tiles of the item
-    int64_t last = c0;
-    if (nt > 0) last = (re * workers - 1) / total;  // the share that holds the item's last tile
-    for (int r = blockIdx.y * kAt + warp / kSplit; r < rows; r += gridDim.y * kAt) {
-        float mx = -INFINITY, sum = 0.f, acc[8];
+    for (int64_t cb = c0 + warp; cb <= last; cb += kMergeWarps * kAhead) {
+        float w[kAhead], x[kAhead][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-        if (nt > 0) {
-            auto piece_of = [&](int64_t c) -> int64_t {  // -1: an empty share
-                if (c == c0) return 2 * c0 + 1;
-                return share_start(c + 1, total, workers) > share_start(c, total, workers) ? 2 * c : -1;
-            };
-            for (int64_t c = c0 + lane; c <= last; c += 32) {
-                const int64_t p = piece_of(c);
-                if (p >= 0) mx = fmaxf(mx, lse[p * kRows + r]);
-            }
+        for (int u = 0; u < kAhead; ++u) {
+            const int64_t c = cb + u * kMergeWarps;
+            const bool have = c <= last && (c == c0 || share_start(c + 1, total, workers) > share_start(c, total, workers));
+            const int64_t p = c == c0 ? 2 * c0 + 1 : 2 * c;
+            w[u] = -INFINITY;
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            if (mx == -INFINITY) mx = 0.f;  // nothing visible (or only NaNs, which stay)
-            constexpr int kAhead = 4;
-            for (int64_t cb = c0 + warp % kSplit; cb <= last; cb += kSplit * kAhead) {
-                float w[kAhead], x[kAhead][8];
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const int64_t c = cb + u * kSplit;
-                    const int64_t p = c <= last ? piece_of(c) : -1;
-                    w[u] = p >= 0 ? lse[p * kRows + r] : -INFINITY;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[u][j] = 0.f;
-                    if (p >= 0) {
-                        const float4 *src = reinterpret_cast<const float4 *>(a.ws + (p * kRows + r) * kD + lane * 8);
-                        *reinterpret_cast<float4 *>(&x[u][0]) = __ldcs(src);
-                        *reinterpret_cast<float4 *>(&x[u][4]) = __ldcs(src + 1);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < kAhead; ++u) {
-                    const float f = exp2f(w[u] - mx);
-                    sum += f;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[j] = fmaf(f, x[u][j], acc[j]);
-                }
-            }
-            if (kSplit > 1) {
-                __syncthreads();
-#pragma unroll
-                for (int j = 0; j < 8; ++j) part[warp][lane * 8 + j] = acc[j];
-                if (lane == 0) part[warp][kD] = sum;
-                __syncthreads();
-                if (warp % kSplit == 0) {
-                    for (int w = 1; w < kSplit; ++w) {
-                        sum += part[warp + w][kD];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) acc[j] += part[warp + w][lane * 8 + j];
-                    }
-                }
+            for (int j = 0; j < 8; ++j) x[u][j] = 0.f;
+            if (have) {
+                w[u] = lse[p * kRows + r];
+                const float4 *src = reinterpret_cast<const float4 *>(a.ws + (p * kRows + r) * kD + lane * 8);
+                *reinterpret_cast<float4 *>(&x[u][0]) = __ldcs(src);
+                *reinterpret_cast<float4 *>(&x[u][4]) = __ldcs(src + 1);
             }
         }
-        if (kSplit > 1 && warp % kSplit != 0) continue;
-        const bool none = sum == 0.f;
-        const float inv = none ? 0.f : 1.f / sum;
-        const int64_t row = (g.row0 + r / kGrp) * kHQ + hd * kGrp + r % kGrp;
-        __nv_bfloat162 h[4];
+        float m = mx;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            h[j] = __floats2bfloat162_rn(none ? 0.f : acc[2 * j] * inv, none ? 0.f : acc[2 * j + 1] * inv);
-        *reinterpret_cast<uint4 *>(a.o + row * kD + lane * 8) = *reinterpret_cast<const uint4 *>(h);
-        if (a.lse != nullptr && lane == 0)
-            a.lse[row] = none ? -INFINITY : (mx + log2f(sum)) * 0.6931471805599453f;
+        for (int u = 0; u < kAhead; ++u) m = fmaxf(m, w[u]);
+        const float base = m == -INFINITY ? 0.f : m;  // nothing visible (or only NaNs, which stay)
+        const float f = exp2f(mx - base);
+        mx = m;
+        sum *= f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[j] *= f;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const float e = exp2f(w[u] - base);
+            sum += e;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[j] = fmaf(e, x[u][j], acc[j]);
+        }
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[warp][lane * 8 + j] = acc[j];
+    if (lane == 0) {
+        part[warp][kD] = sum;
+        part[warp][kD + 1] = mx;
+    }
+    __syncthreads();
+    const int d = threadIdx.x;  // kMergeThreads = kD: a dim each
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, part[w][kD + 1]);
+    const float base = top == -INFINITY ? 0.f : top;
+    float L = 0.f, o = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMergeWarps; ++w) {
+        const float f = exp2f(part[w][kD + 1] - base);
+        L = fmaf(f, part[w][kD], L);
+        o = fmaf(f, part[w][d], o);
+    }
+    const bool none = L == 0.f;
+    const int64_t row = (g.row0 + r / kGrp) * kHQ + hd * kGrp + r % kGrp;
+    a.o[row * kD + d] = __float2bfloat16_rn(none ? 0.f : o / L);
+    if (a.lse != nullptr && d == 0) a.lse[row] = none ? -INFINITY : (top + log2f(L)) * 0.6931471805599453f;
 }
 
-// The same for many rows and few pieces each: a warp per kPer rows, in one pass over the pieces.
+// The same for many rows and few pieces each: a warp per kPer rows, with the tiles' prefix that the
+// attention kernel leaves.
 template <int kTok, int kKeys, int kPer>
 __global__ void __launch_bounds__(kMergeThreads)
 chunk_merge_many_kernel(const ChunkArgs a, const int64_t *__restrict__ prefix, int64_t workers)
@@ -337,8 +354,8 @@ cudaError_t launch_chunk_merge(const ChunkArgs &a, const int64_t *prefix, int64_
     if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
     // few rows: a CTA per row, its eight warps over the row's pieces; many: a warp per four rows
     if (items * kRows <= 4096)
-        return launch_pdl(chunk_merge_kernel<kTok, kKeys, 8>, dim3((unsigned)items, kRows), dim3(kMergeThreads), 0,
-                          stream, a, prefix, workers);
+        return launch_pdl(chunk_merge_kernel<kTok, kKeys>, dim3((unsigned)items, kRows), dim3(kMergeThreads), 0, stream, a,
+                          workers);
     constexpr int kPer = 4, kBlock = kMergeWarps * kPer;
     return launch_pdl(chunk_merge_many_kernel<kTok, kKeys, kPer>, dim3((unsigned)items, (kRows + kBlock - 1) / kBlock),
                       dim3(kMergeThreads), 0, stream, a, prefix, workers);
