@@ -48,7 +48,7 @@ struct DecCfg {
     static constexpr int kOffScale = kOffStats + 2 * kDecWarps * 16 * (int)sizeof(float);
     static constexpr int kSmem = kOffScale + 16 * (int)sizeof(float);
     static_assert(kDecWarps * kGrp * kMergePitch * 4 <= kDecWarps * kRing * kSlot, "the merge reuses the ring");
-    static_assert(kSmem <= 232448 - 1024, "shared memory of one CTA");
+    static_assert(kSmem + 2048 <= 232448, "shared memory of one CTA");
 };
 
 template <bool kHalf>
@@ -118,23 +118,26 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ ChunkShare share;
     __shared__ int64_t scan[kDecWarps];
+    __shared__ ChunkLengths lengths;
     pdl_enter();
+    lengths.fill(a);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n = lane >> 2, c = lane & 3;  // fragment coordinates
     uint4 *sq = reinterpret_cast<uint4 *>(smem);
     float *stats = reinterpret_cast<float *>(smem + C::kOffStats);  // [maximum, sum][warp][16 rows]
     float *states = reinterpret_cast<float *>(smem + C::kOffRing);  // [warp][12 rows][kMergePitch], at an item's end
     const uint32_t ring = smem_u32(smem + C::kOffRing) + warp * C::kRing * C::kSlot;
-    chunk_share<1, kDecKeys, kDecThreads>(a, blockIdx.x, gridDim.x, &share, scan, blockIdx.x == 0 ? prefix : nullptr);
+    chunk_share<1, kDecKeys, kDecThreads>(a, blockIdx.x, gridDim.x, &share, scan, blockIdx.x == 0 ? prefix : nullptr,
+                                              &lengths);
     int64_t at = share.ts, slot = share.slot, first = share.first;
     const int64_t te = share.te;
     const float c2 = a.scale * 1.4426950408889634f;
 
     while (at < te) {
-        ChunkGroup g = chunk_group<1, kDecKeys>(a, slot);
+        ChunkGroup g = chunk_group<1, kDecKeys>(a, slot, &lengths);
         while (at >= first + 2 * (int64_t)g.nt) {  // empty slots between two tokens
             first += 2 * (int64_t)g.nt;
-            g = chunk_group<1, kDecKeys>(a, ++slot);
+            g = chunk_group<1, kDecKeys>(a, ++slot, &lengths);
         }
         const int hd = at >= first + g.nt ? 1 : 0;  // KV head
         const int64_t item = first + (int64_t)hd * g.nt;

@@ -52,6 +52,7 @@ struct TcShared {
     int abort_flag;
     int64_t scan[16], walk[16][3];
     ChunkShare share;
+    ChunkLengths lengths;
 };
 
 struct TcTable {  // e4m3: pool rows (of the KV head, -1: none) and scale bytes of a tile's keys
@@ -255,7 +256,7 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane)
 
 // The items of a share, in order: every role walks the same list.
 struct TcWalk {
-    const ChunkShare *share;
+    const TcShared *sh;
     int64_t *state;  // shared memory, of this warp: next tile, its group's slot and that slot's first tile
     // the current item
     int s, nq, nt, ns, w_tile;  // as in its ChunkGroup
@@ -265,12 +266,12 @@ struct TcWalk {
     int near, sinks;      // some row sees the keys near .. t_last and those below sinks
     const int32_t *table; // the sequence's row of the block table
 
-    __device__ __forceinline__ TcWalk(const ChunkShare *sh, int64_t *st) : share(sh), state(st)
+    __device__ __forceinline__ TcWalk(const TcShared *shared, int64_t *st) : sh(shared), state(st)
     {
         if ((threadIdx.x & 31) == 0) {
-            st[0] = sh->ts;
-            st[1] = sh->slot;
-            st[2] = sh->first;
+            st[0] = sh->share.ts;
+            st[1] = sh->share.slot;
+            st[2] = sh->share.first;
         }
         __syncwarp();
     }
@@ -279,12 +280,12 @@ struct TcWalk {
     __device__ __forceinline__ bool next(const ChunkArgs &a)
     {
         int64_t at = state[0], slot = state[1], first = state[2];
-        const int64_t te = share->te;
+        const int64_t te = sh->share.te;
         if (at >= te) return false;
-        ChunkGroup g = chunk_group<kTcTok, kTcKeys>(a, slot);
+        ChunkGroup g = chunk_group<kTcTok, kTcKeys>(a, slot, &sh->lengths);
         while (at >= first + 2 * (int64_t)g.nt) {  // empty slots between two groups
             first += 2 * (int64_t)g.nt;
-            g = chunk_group<kTcTok, kTcKeys>(a, ++slot);
+            g = chunk_group<kTcTok, kTcKeys>(a, ++slot, &sh->lengths);
         }
         hd = at >= first + g.nt ? 1 : 0;
         const int64_t item = first + (int64_t)hd * g.nt;
@@ -391,7 +392,8 @@ __device__ __forceinline__ void codes_to_slot(const uint4 &codes, const RowScale
 
 template <bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcCfg<kFp8>::kThreads, 1)
-chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, int64_t *__restrict__ prefix)
+chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_q4,
+                const ChunkArgs a, int64_t *__restrict__ prefix)
 {
     using C = TcCfg<kFp8>;
     extern __shared__ uint8_t smem_raw[];
@@ -430,15 +432,16 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
                      ::"r"(smem_u32(&sh->tmem_base)), "r"(kTcCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    sh->lengths.fill(a);
     chunk_share<kTcTok, kTcKeys, C::kThreads>(a, worker, workers, &sh->share, sh->scan,
-                                              blockIdx.x == 0 ? prefix : nullptr);
+                                              blockIdx.x == 0 ? prefix : nullptr, &sh->lengths);
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // both CTAs' barriers are initialised
     tc_fence_after();
     const uint32_t tmem = sh->tmem_base;
     volatile int *abort_flag = &sh->abort_flag;
-    TcWalk it(&sh->share, sh->walk[warp]);
+    TcWalk it(sh, sh->walk[warp]);
     bool ok = true;
     if (warp == 0) {
         // ---------------- Q ----------------
@@ -446,13 +449,26 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const ChunkArgs a, in
         while (ok && it.next(a)) {
             ok = mbar_wait(&sh->q_empty, (n & 1) ^ 1, abort_flag);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            if (lane == 0) mbar_arrive_expect_tx(&sh->q_full, kTcQ);
-            __syncwarp();
-            const int row = (int)rank * 128 + lane * 4, tok = row / kGrp;
-            const int32_t y = tok < it.nq ? (int32_t)(it.row0 + tok) : (int32_t)a.total_q;  // outside: zeros
+            // CTA 0: tokens 0 .. 9 and heads 0 .. 7 of token 10, CTA 1: its other heads and tokens 11 .. 20 (what
+            // lies behind the group's tokens is not written, and zeros come from behind the tensor).  In few
+            // copies: one of 4 rows takes the 75 cycles of a longer one.
+            if (lane == 0) {
+                const int g = it.hd * kGrp;
+                mbar_arrive_expect_tx(&sh->q_full, (rank == 0 ? 128 : 124) * kD * 2);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                tma_load_3d(sQ + c * kTcQChunk + lane * 512, &map_q, &sh->q_full, c * 64, it.hd * kGrp + row % kGrp, y);
+                for (int c = 0; c < 4; ++c) {
+                    uint8_t *dst = sQ + c * kTcQChunk;
+                    if (rank == 0) {
+                        tma_load_3d(dst, &map_q, &sh->q_full, c * 64, g, it.row0);
+                        tma_load_3d(dst + 120 * 128, &map_q4, &sh->q_full, c * 64, g, it.row0 + 10);
+                        tma_load_3d(dst + 124 * 128, &map_q4, &sh->q_full, c * 64, g + 4, it.row0 + 10);
+                    } else {
+                        tma_load_3d(dst, &map_q4, &sh->q_full, c * 64, g + 8, it.row0 + 10);
+                        tma_load_3d(dst + 4 * 128, &map_q, &sh->q_full, c * 64, g, it.row0 + 11);
+                    }
+                }
+            }
+            __syncwarp();
             ++n;
         }
     } else if (warp == 1) {
@@ -972,8 +988,9 @@ size_t tc_prefix_offset() { return (size_t)(2 * kTcMaxPairs) * kTcRows * (kD + 1
 template <bool kFp8>
 cudaError_t launch_tc(const ChunkArgs &a, cudaStream_t stream)
 {
-    CUtensorMap mq;
-    if (!make_tmap_3d(&mq, a.q, kD, kHQ, (uint64_t)a.total_q, kD * 2, (uint64_t)kHQ * kD * 2, 64, 4, 1))
+    CUtensorMap mq, mq4;  // ten tokens, and four heads of one, of 64 dims
+    if (!make_tmap_3d(&mq, a.q, kD, kHQ, (uint64_t)a.total_q, kD * 2, (uint64_t)kHQ * kD * 2, 64, kGrp, 10) ||
+        !make_tmap_3d(&mq4, a.q, kD, kHQ, (uint64_t)a.total_q, kD * 2, (uint64_t)kHQ * kD * 2, 64, 4, 1))
         return cudaErrorInvalidValue;
     cudaError_t e = set_smem_attr_once(reinterpret_cast<const void *>(chunk_tc_kernel<kFp8>), TcCfg<kFp8>::kSmem);
     if (e != cudaSuccess) return e;
@@ -982,7 +999,7 @@ cudaError_t launch_tc(const ChunkArgs &a, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     int64_t *prefix = reinterpret_cast<int64_t *>(reinterpret_cast<uint8_t *>(a.ws) + tc_prefix_offset());
     e = launch_pdl(chunk_tc_kernel<kFp8>, dim3((unsigned)(2 * workers)), dim3(TcCfg<kFp8>::kThreads), TcCfg<kFp8>::kSmem,
-                   stream, mq, a, prefix);
+                   stream, mq, mq4, a, prefix);
     if (e != cudaSuccess) return e;
     return launch_chunk_merge<kTcTok, kTcKeys>(a, prefix, workers, stream);
 }

@@ -41,26 +41,45 @@ __device__ __forceinline__ int64_t tile_start(const ChunkGroup &g, int i, int ke
     return (i < g.ns ? (int64_t)i : g.w_tile + (i - g.ns)) * keys;
 }
 
+// A batch's lengths in shared memory (up to kCuBatch sequences), for the searches of every role and item.
+constexpr int kCuBatch = 128;
+struct ChunkLengths {
+    int32_t q[kCuBatch + 1], k[kCuBatch + 1];
+
+    __device__ __forceinline__ void fill(const ChunkArgs &a)  // by the whole CTA
+    {
+        if (a.batch <= kCuBatch)
+            for (int i = threadIdx.x; i <= a.batch; i += blockDim.x) {
+                q[i] = __ldg(a.cu_q + i);
+                k[i] = __ldg(a.cu_k + i);
+            }
+        __syncthreads();
+    }
+};
+
 template <int kTok, int kKeys>
-__device__ __forceinline__ ChunkGroup chunk_group(const ChunkArgs &a, int64_t slot)
+__device__ __forceinline__ ChunkGroup chunk_group(const ChunkArgs &a, int64_t slot, const ChunkLengths *sh = nullptr)
 {
+    const bool local = sh != nullptr && a.batch <= kCuBatch;
+    auto cu_q = [&](int i) -> int32_t { return local ? sh->q[i] : __ldg(a.cu_q + i); };
+    auto cu_k = [&](int i) -> int32_t { return local ? sh->k[i] : __ldg(a.cu_k + i); };
     ChunkGroup g;
     g.nt = g.ns = g.nq = 0;
     g.w_tile = g.row0 = g.t0 = 0;
     int lo = 0, hi = a.batch;  // the last s whose first slot is <= slot
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((int64_t)(__ldg(a.cu_q + mid) / kTok) + mid <= slot) lo = mid; else hi = mid;
+        if ((int64_t)(cu_q(mid) / kTok) + mid <= slot) lo = mid; else hi = mid;
     }
     g.s = lo;
-    const int64_t q0 = __ldg(a.cu_q + lo), q1 = __ldg(a.cu_q + lo + 1);
+    const int64_t q0 = cu_q(lo), q1 = cu_q(lo + 1);
     const int64_t first = (slot - (q0 / kTok + lo)) * kTok, Lq = q1 - q0;
     if (q0 < 0 || first < 0 || first >= Lq) return g;
     if (q1 > a.total_q) {  // lengths that the query tensor does not hold
         set_device_status(QSA_ERR_DEVICE_CHECK);
         return g;
     }
-    const int64_t Lk = (int64_t)__ldg(a.cu_k + lo + 1) - __ldg(a.cu_k + lo);
+    const int64_t Lk = (int64_t)cu_k(lo + 1) - cu_k(lo);
     g.nq = (int)(Lq - first < kTok ? Lq - first : kTok);
     g.row0 = q0 + first;
     g.t0 = Lk - Lq + first;
@@ -91,14 +110,18 @@ struct ChunkShare {
 };
 
 // first tile of share c
-__device__ __forceinline__ int64_t share_start(int64_t c, int64_t total, int64_t workers) { return c * total / workers; }
+__device__ __forceinline__ int64_t share_start(int64_t c, int64_t total, int64_t workers)
+{
+    const int64_t x = c * total;
+    return x < ((int64_t)1 << 32) ? (int64_t)((uint32_t)x / (uint32_t)workers) : x / workers;
+}
 
 // This worker's share, by the whole CTA (threads a power of two of whole warps); `scan`: a
 // shared array of one entry per warp.  `prefix` (worker 0's CTA, or null): the first tile
 // of every slot and, behind them, the total, for the merge.
 template <int kTok, int kKeys, int kThreads>
 __device__ __forceinline__ void chunk_share(const ChunkArgs &a, int64_t worker, int64_t workers, ChunkShare *out,
-                                            int64_t *scan, int64_t *prefix)
+                                            int64_t *scan, int64_t *prefix, const ChunkLengths *sh)
 {
     constexpr int kWarps = kThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -106,7 +129,7 @@ __device__ __forceinline__ void chunk_share(const ChunkArgs &a, int64_t worker, 
     const int64_t per = (slots + kThreads - 1) / kThreads;  // consecutive slots of a thread
     const int64_t u0 = tid * per < slots ? tid * per : slots, u1 = u0 + per < slots ? u0 + per : slots;
     int64_t mine = 0;
-    for (int64_t u = u0; u < u1; ++u) mine += kHKV * (int64_t)chunk_group<kTok, kKeys>(a, u).nt;
+    for (int64_t u = u0; u < u1; ++u) mine += kHKV * (int64_t)chunk_group<kTok, kKeys>(a, u, sh).nt;
     int64_t incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -132,7 +155,7 @@ __device__ __forceinline__ void chunk_share(const ChunkArgs &a, int64_t worker, 
     if (holds || prefix != nullptr) {
         int64_t at = before;
         for (int64_t u = u0; u < u1; ++u) {
-            const int64_t n = kHKV * (int64_t)chunk_group<kTok, kKeys>(a, u).nt;
+            const int64_t n = kHKV * (int64_t)chunk_group<kTok, kKeys>(a, u, sh).nt;
             if (prefix != nullptr) prefix[u] = at;
             if (holds && at <= ts && ts < at + n) {
                 out->slot = u;
