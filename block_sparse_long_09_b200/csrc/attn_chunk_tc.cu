@@ -34,13 +34,12 @@ namespace qsa {
 
 namespace {
 
-constexpr int kTcTok = 21, kTcRows = kTcTok * kGrp, kTcKeys = 128;
 constexpr int kTcSlot = 32768, kTcMaxStages = 5, kTcTables = 4;
 constexpr int kTcQ = 128 * kD * 2;
-constexpr int kTcQChunk = 128 * 128, kTcKChunk = 64 * 128, kTcVChunk = 128 * 128;
+constexpr int kTcQChunk = 128 * 128, kTcKChunk = 64 * 128;
 constexpr uint32_t kTcO = 256, kTcCols = 512;
 constexpr float kTcRescale = 8.f;
-constexpr int64_t kTcMaxPairs = 80;
+constexpr int64_t kTcMaxPairs = 80, kTcMaxSingles = 160;
 
 struct TcShared {
     uint64_t kv_full[kTcMaxStages], kv_peer[kTcMaxStages], kv_empty[kTcMaxStages];
@@ -55,19 +54,22 @@ struct TcShared {
     ChunkLengths lengths;
 };
 
+template <int kCtas>
 struct TcTable {  // e4m3: pool rows (of the KV head, -1: none) and scale bytes of a tile's keys
-    int32_t row[kTcTables][kTcKeys];
-    uint8_t ks[kTcTables][kTcKeys], vs[kTcTables][kTcKeys];
+    int32_t row[kTcTables][64 * kCtas];
+    uint8_t ks[kTcTables][64 * kCtas], vs[kTcTables][64 * kCtas];
 };
 
-template <bool kFp8>
+template <bool kFp8, int kCtas>
 struct TcCfg {
+    static constexpr int kTok = kCtas == 2 ? 21 : 10, kRows = kTok * kGrp, kKeys = 64 * kCtas;
+    static constexpr int kVChunks = 4 / kCtas, kVChunk = kKeys * 128;  // 64 dims of a V tile
     static constexpr int kThreads = kFp8 ? 512 : 256;
     static constexpr int kStages = kFp8 ? 4 : 5;
     static constexpr int kFills = kFp8 ? 8 : 64;  // arrivals that fill a slot: warps that convert, threads that copy
     static constexpr int kOffRing = kTcQ;
     static constexpr int kOffTable = kOffRing + kStages * kTcSlot;
-    static constexpr int kOffShared = kOffTable + (kFp8 ? (int)sizeof(TcTable) : 0);
+    static constexpr int kOffShared = kOffTable + (kFp8 ? (int)sizeof(TcTable<kCtas>) : 0);
     static constexpr int kSmem = kOffShared + (int)sizeof(TcShared) + 1024;
     static_assert(kSmem <= 232448, "shared memory of one CTA");
 };
@@ -145,9 +147,14 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool have)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have ? 16 : 0) : "memory");
 }
 
-// D (+)= A B^T over the pair, A from shared memory or from TMEM
-__device__ __forceinline__ void mma2_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+// D (+)= A B^T over the item's CTAs, A from shared memory or from TMEM
+template <int kCtas>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
+    if (kCtas == 1) {
+        mma_bf16_ss(d, a, b, idesc, accumulate);
+        return;
+    }
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
@@ -155,18 +162,31 @@ __device__ __forceinline__ void mma2_ss(uint32_t d, uint64_t a, uint64_t b, uint
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-__device__ __forceinline__ void mma2_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+template <int kCtas>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
-        ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+    if (kCtas == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+            ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n"
+            ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 
-// arrive on the barrier of both CTAs once this thread's tcgen05 operations have completed
-__device__ __forceinline__ void commit_both(uint64_t *bar)
+// arrive on the barrier of the item's CTAs once this thread's tcgen05 operations have completed
+template <int kCtas>
+__device__ __forceinline__ void commit_all(uint64_t *bar)
 {
+    if (kCtas == 1) {
+        mma_commit(bar);
+        return;
+    }
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
         ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
@@ -255,6 +275,7 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane)
 }
 
 // The items of a share, in order: every role walks the same list.
+template <int kTok, int kKeys>
 struct TcWalk {
     const TcShared *sh;
     int64_t *state;  // shared memory, of this warp: next tile, its group's slot and that slot's first tile
@@ -282,10 +303,10 @@ struct TcWalk {
         int64_t at = state[0], slot = state[1], first = state[2];
         const int64_t te = sh->share.te;
         if (at >= te) return false;
-        ChunkGroup g = chunk_group<kTcTok, kTcKeys>(a, slot, &sh->lengths);
+        ChunkGroup g = chunk_group<kTok, kKeys>(a, slot, &sh->lengths);
         while (at >= first + 2 * (int64_t)g.nt) {  // empty slots between two groups
             first += 2 * (int64_t)g.nt;
-            g = chunk_group<kTcTok, kTcKeys>(a, ++slot, &sh->lengths);
+            g = chunk_group<kTok, kKeys>(a, ++slot, &sh->lengths);
         }
         hd = at >= first + g.nt ? 1 : 0;
         const int64_t item = first + (int64_t)hd * g.nt;
@@ -312,7 +333,7 @@ struct TcWalk {
     }
 
     // first key of tile i
-    __device__ __forceinline__ int tile(int i) const { return (i < ns ? i : w_tile + (i - ns)) * kTcKeys; }
+    __device__ __forceinline__ int tile(int i) const { return (i < ns ? i : w_tile + (i - ns)) * kKeys; }
 
     // does any row of the item see key j
     __device__ __forceinline__ bool any_sees(int j) const
@@ -390,19 +411,20 @@ __device__ __forceinline__ void codes_to_slot(const uint4 &codes, const RowScale
                      : "memory");
 }
 
-template <bool kFp8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(TcCfg<kFp8>::kThreads, 1)
+template <bool kFp8, int kCtas>
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__((TcCfg<kFp8, kCtas>::kThreads), 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_q4,
                 const ChunkArgs a, int64_t *__restrict__ prefix)
 {
-    using C = TcCfg<kFp8>;
+    using C = TcCfg<kFp8, kCtas>;
+    constexpr int kKeys = C::kKeys;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sQ = smem, *ring = smem + C::kOffRing;
     TcShared *sh = reinterpret_cast<TcShared *>(smem + C::kOffShared);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cta_rank();
-    const int64_t worker = blockIdx.x >> 1, workers = gridDim.x >> 1;
+    const int64_t worker = blockIdx.x / kCtas, workers = gridDim.x / kCtas;
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&sh->kv_full[i], C::kFills);
@@ -414,11 +436,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
         mbar_init(&sh->q_empty, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh->s_full[i], 1);
-            mbar_init(&sh->p_full[i], 8);
+            mbar_init(&sh->p_full[i], 4 * kCtas);
         }
         mbar_init(&sh->pv_done, 1);
         mbar_init(&sh->o_full, 1);
-        mbar_init(&sh->o_empty, 8);
+        mbar_init(&sh->o_empty, 4 * kCtas);
         for (int i = 0; i < kTcTables; ++i) {
             mbar_init(&sh->tab_full[i], 2);
             mbar_init(&sh->tab_empty[i], 8);
@@ -428,20 +450,25 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
     }
     pdl_enter();  // before the allocation: no CTA waits while it holds tensor memory
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
-                     ::"r"(smem_u32(&sh->tmem_base)), "r"(kTcCols) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        if (kCtas == 1) {
+            tmem_alloc(&sh->tmem_base, kTcCols);
+            tmem_relinquish();
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                         ::"r"(smem_u32(&sh->tmem_base)), "r"(kTcCols) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        }
     }
     sh->lengths.fill(a);
-    chunk_share<kTcTok, kTcKeys, C::kThreads>(a, worker, workers, &sh->share, sh->scan,
+    chunk_share<C::kTok, kKeys, C::kThreads>(a, worker, workers, &sh->share, sh->scan,
                                               blockIdx.x == 0 ? prefix : nullptr, &sh->lengths);
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // both CTAs' barriers are initialised
+    if (kCtas == 2) cluster_sync();  // both CTAs' barriers are initialised
     tc_fence_after();
     const uint32_t tmem = sh->tmem_base;
     volatile int *abort_flag = &sh->abort_flag;
-    TcWalk it(sh, sh->walk[warp]);
+    TcWalk<C::kTok, kKeys> it(sh, sh->walk[warp]);
     bool ok = true;
     if (warp == 0) {
         // ---------------- Q ----------------
@@ -449,19 +476,21 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
         while (ok && it.next(a)) {
             ok = mbar_wait(&sh->q_empty, (n & 1) ^ 1, abort_flag);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            // CTA 0: tokens 0 .. 9 and heads 0 .. 7 of token 10, CTA 1: its other heads and tokens 11 .. 20 (what
-            // lies behind the group's tokens is not written, and zeros come from behind the tensor).  In few
-            // copies: one of 4 rows takes the 75 cycles of a longer one.
+            // Ten tokens, or of 21 CTA 0 the tokens 0 .. 9 and heads 0 .. 7 of token 10, CTA 1 its other heads and
+            // the tokens 11 .. 20 (what lies behind the group's tokens is not written, and zeros come from
+            // behind the tensor).  In few copies: one of 4 rows takes the 75 cycles of a longer one.
             if (lane == 0) {
                 const int g = it.hd * kGrp;
-                mbar_arrive_expect_tx(&sh->q_full, (rank == 0 ? 128 : 124) * kD * 2);
+                mbar_arrive_expect_tx(&sh->q_full, (kCtas == 1 ? 120 : (rank == 0 ? 128 : 124)) * kD * 2);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint8_t *dst = sQ + c * kTcQChunk;
                     if (rank == 0) {
                         tma_load_3d(dst, &map_q, &sh->q_full, c * 64, g, it.row0);
-                        tma_load_3d(dst + 120 * 128, &map_q4, &sh->q_full, c * 64, g, it.row0 + 10);
-                        tma_load_3d(dst + 124 * 128, &map_q4, &sh->q_full, c * 64, g + 4, it.row0 + 10);
+                        if (kCtas == 2) {
+                            tma_load_3d(dst + 120 * 128, &map_q4, &sh->q_full, c * 64, g, it.row0 + 10);
+                            tma_load_3d(dst + 124 * 128, &map_q4, &sh->q_full, c * 64, g + 4, it.row0 + 10);
+                        }
                     } else {
                         tma_load_3d(dst, &map_q4, &sh->q_full, c * 64, g + 8, it.row0 + 10);
                         tma_load_3d(dst + 4 * 128, &map_q, &sh->q_full, c * 64, g, it.row0 + 11);
@@ -482,51 +511,51 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
             };
             if (rank == 0) {
                 // ---------------- products ----------------
-                constexpr uint32_t idesc_s = idesc_bf16_f32(256, kTcKeys, 0, 0);
-                constexpr uint32_t idesc_o = idesc_bf16_f32(256, kD, 0, 1);
+                constexpr uint32_t idesc_s = idesc_bf16_f32(128 * kCtas, kKeys, 0, 0);
+                constexpr uint32_t idesc_o = idesc_bf16_f32(128 * kCtas, kD, 0, 1);
                 const uint32_t q_addr = smem_u32(sQ), ring_u = smem_u32(ring);
                 uint32_t T = 0;  // tiles so far
                 auto slot_full = [&]() -> bool {
                     if (!mbar_wait(&sh->kv_full[stage], ph, abort_flag)) return false;
                     fence_proxy_async_smem();
-                    return wait_pair(&sh->kv_peer[stage], ph, abort_flag);
+                    return kCtas == 1 || wait_pair(&sh->kv_peer[stage], ph, abort_flag);
                 };
                 auto do_s = [&](uint32_t t) -> bool {
                     if (!slot_full()) return false;
                     tc_fence_after();
-                    const uint32_t k_addr = ring_u + stage * kTcSlot, d = tmem + (t & 1) * kTcKeys;
+                    const uint32_t k_addr = ring_u + stage * kTcSlot, d = tmem + (t & 1) * kKeys;
 #pragma unroll
                     for (int ks = 0; ks < kD / 16; ++ks)
-                        mma2_ss(d, sdesc_sw128(q_addr + (ks >> 2) * kTcQChunk + (ks & 3) * 32, 16, 1024),
+                        mma_ss<kCtas>(d, sdesc_sw128(q_addr + (ks >> 2) * kTcQChunk + (ks & 3) * 32, 16, 1024),
                                 sdesc_sw128(k_addr + (ks >> 2) * kTcKChunk + (ks & 3) * 32, 16, 1024), idesc_s,
                                 ks > 0 ? 1u : 0u);
-                    commit_both(&sh->kv_empty[stage]);
-                    commit_both(&sh->s_full[t & 1]);
+                    commit_all<kCtas>(&sh->kv_empty[stage]);
+                    commit_all<kCtas>(&sh->s_full[t & 1]);
                     advance();
                     return true;
                 };
                 while (ok && it.next(a)) {
                     const int nt = it.i1 - it.i0;
-                    ok = wait_pair(&sh->q_full, n & 1, abort_flag) && wait_pair(&sh->q_peer, n & 1, abort_flag);
+                    ok = mbar_wait(&sh->q_full, n & 1, abort_flag) && (kCtas == 1 || wait_pair(&sh->q_peer, n & 1, abort_flag));
                     ok = ok && do_s(T);
-                    if (ok && nt == 1) commit_both(&sh->q_empty);
+                    if (ok && nt == 1) commit_all<kCtas>(&sh->q_empty);
                     for (int i = 0; ok && i < nt; ++i, ++T) {
                         if (i + 1 < nt) {
                             if (!(ok = do_s(T + 1))) break;
-                            if (i + 2 == nt) commit_both(&sh->q_empty);
+                            if (i + 2 == nt) commit_all<kCtas>(&sh->q_empty);
                         }
                         if (i == 0 && !(ok = wait_pair(&sh->o_empty, (n & 1) ^ 1, abort_flag))) break;
                         if (!(ok = wait_pair(&sh->p_full[T & 1], (T >> 1) & 1, abort_flag))) break;
                         if (!(ok = slot_full())) break;
                         tc_fence_after();
-                        const uint32_t v_addr = ring_u + stage * kTcSlot, p = tmem + (T & 1) * kTcKeys;
+                        const uint32_t v_addr = ring_u + stage * kTcSlot, p = tmem + (T & 1) * kKeys;
 #pragma unroll
-                        for (int ks = 0; ks < kTcKeys / 16; ++ks)
-                            mma2_ts(tmem + kTcO, p + ks * 8, sdesc_sw128(v_addr + ks * 2048, kTcVChunk, 1024), idesc_o,
+                        for (int ks = 0; ks < kKeys / 16; ++ks)
+                            mma_ts<kCtas>(tmem + kTcO, p + ks * 8, sdesc_sw128(v_addr + ks * 2048, C::kVChunk, 1024), idesc_o,
                                     (i == 0 && ks == 0) ? 0u : 1u);
-                        commit_both(&sh->kv_empty[stage]);
-                        commit_both(&sh->pv_done);
-                        if (i + 1 == nt) commit_both(&sh->o_full);
+                        commit_all<kCtas>(&sh->kv_empty[stage]);
+                        commit_all<kCtas>(&sh->pv_done);
+                        if (i + 1 == nt) commit_all<kCtas>(&sh->o_full);
                         advance();
                     }
                     ++n;
@@ -552,8 +581,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
     } else if (warp < 4) {
         if (!kFp8) {
             // ---------------- bf16 K and V ----------------
-            // Warp w copies K of the keys 32 w .. of the CTA's 64, and V of these and of the same keys of
-            // the other CTA's 64; a lane looks up one key of each (row of the KV head, -1: none).  A slot's
+            // Warp w copies K of the keys 32 w .. of the CTA's 64, and V of these and, in a pair, of the same keys
+            // of the other CTA's 64; a lane looks up one key of each (row of the KV head, -1: none).  A slot's
             // barrier counts the threads whose copies have arrived.
             const int w = warp - 2, u = lane & 7, k4 = lane >> 3;
             const uint32_t ring_u = smem_u32(ring);
@@ -573,17 +602,17 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                 }
             };
             while (ok && it.next(a)) {
-                int32_t page[2];
-                uint32_t off[2] = {0u, 0u};
+                int32_t page[kCtas];
+                uint32_t off[kCtas] = {};
                 auto fetch = [&](int i) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) page[e] = it.page_of(a, i, ((int)rank ^ e) * 64 + w * 32 + lane, &off[e]);
+                    for (int e = 0; e < kCtas; ++e) page[e] = it.page_of(a, i, ((int)rank ^ e) * 64 + w * 32 + lane, &off[e]);
                 };
-                auto resolve = [&](int32_t (&r)[2]) {
+                auto resolve = [&](int32_t (&r)[kCtas]) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) r[e] = it.row_of(a, page[e], off[e]);
+                    for (int e = 0; e < kCtas; ++e) r[e] = it.row_of(a, page[e], off[e]);
                 };
-                auto load_k = [&](const int32_t (&r)[2]) -> bool {
+                auto load_k = [&](const int32_t (&r)[kCtas]) -> bool {
                     if (!slot_ready()) return false;
                     const uint32_t dst = ring_u + stage * kTcSlot + (w * 32 + k4) * 128;
 #pragma unroll
@@ -597,22 +626,22 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                     slot_issued();
                     return true;
                 };
-                auto load_v = [&](const int32_t (&r)[2]) -> bool {
+                auto load_v = [&](const int32_t (&r)[kCtas]) -> bool {
                     if (!slot_ready()) return false;
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) {
+                    for (int x = 0; x < 8 * kCtas; ++x) {
                         const int key = (x & 7) * 4 + k4;
                         const uint32_t dst = ring_u + stage * kTcSlot + (((int)rank ^ (x >> 3)) * 64 + w * 32 + key) * 128;
                         const int32_t row = __shfl_sync(0xffffffffu, r[x >> 3], key);
                         const uint8_t *src = vp + (int64_t)(row < 0 ? 0 : row) * 512;
                         const uint32_t d = dst + (((uint32_t)u ^ (key & 7)) << 4);
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) copy16(d + c * kTcVChunk, src + c * 128, row >= 0);
+                        for (int c = 0; c < C::kVChunks; ++c) copy16(d + c * C::kVChunk, src + c * 128, row >= 0);
                     }
                     slot_issued();
                     return true;
                 };
-                int32_t r0[2], r1[2];
+                int32_t r0[kCtas], r1[kCtas];
                 fetch(it.i0);
                 resolve(r0);
                 fetch(it.i0 + 1);
@@ -623,27 +652,27 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                     if (i + 1 < it.i1) ok = load_k(r1);
                     ok = ok && load_v(r0);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) r0[e] = r1[e];
+                    for (int e = 0; e < kCtas; ++e) r0[e] = r1[e];
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");  // none is on its way when the CTA exits
         } else {
             // ---------------- rows and scales of e4m3 pools ----------------
-            // Two keys per lane; a tile's pages are looked up one tile ahead of its scales, and these
+            // A key or two per lane; a tile's pages are looked up one tile ahead of its scales, and these
             // one ahead of the table's writing.
-            TcTable *tab = reinterpret_cast<TcTable *>(smem + C::kOffTable);
-            const int key = (warp - 2) * 64 + lane;
+            TcTable<kCtas> *tab = reinterpret_cast<TcTable<kCtas> *>(smem + C::kOffTable);
+            const int key = (warp - 2) * 32 * kCtas + lane;
             uint32_t n = 0;  // tables written
             while (ok && it.next(a)) {
-                int32_t page[2], row[2];
-                uint32_t off[2] = {0u, 0u}, kb[2], vb[2];
+                int32_t page[kCtas], row[kCtas];
+                uint32_t off[kCtas] = {}, kb[kCtas], vb[kCtas];
                 auto fetch = [&](int i) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) page[e] = it.page_of(a, i, key + 32 * e, &off[e]);
+                    for (int e = 0; e < kCtas; ++e) page[e] = it.page_of(a, i, key + 32 * e, &off[e]);
                 };
                 auto resolve = [&]() {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
+                    for (int e = 0; e < kCtas; ++e) {
                         row[e] = it.row_of(a, page[e], off[e]);
                         kb[e] = row[e] >= 0 ? __ldg(a.pool.k_scales + row[e]) : 127u;
                         vb[e] = row[e] >= 0 ? __ldg(a.pool.v_scales + row[e]) : 127u;
@@ -653,18 +682,25 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                 resolve();
                 fetch(it.i0 + 1);
                 for (int i = it.i0; i < it.i1; ++i, ++n) {
-                    const int32_t r0 = row[0], r1 = row[1];
-                    const uint32_t k0 = kb[0], k1 = kb[1], v0 = vb[0], v1 = vb[1], x = n % kTcTables;
+                    const uint32_t x = n % kTcTables;
+                    int32_t r[kCtas];
+                    uint32_t k[kCtas], v[kCtas];
+#pragma unroll
+                    for (int e = 0; e < kCtas; ++e) {
+                        r[e] = row[e];
+                        k[e] = kb[e];
+                        v[e] = vb[e];
+                    }
                     resolve();
                     fetch(i + 2);
                     ok = mbar_wait(&sh->tab_empty[x], ((n / kTcTables) & 1) ^ 1, abort_flag);
                     if (!(ok = __all_sync(0xffffffffu, ok))) break;
-                    tab->row[x][key] = r0;
-                    tab->row[x][key + 32] = r1;
-                    tab->ks[x][key] = (uint8_t)k0;
-                    tab->ks[x][key + 32] = (uint8_t)k1;
-                    tab->vs[x][key] = (uint8_t)v0;
-                    tab->vs[x][key + 32] = (uint8_t)v1;
+#pragma unroll
+                    for (int e = 0; e < kCtas; ++e) {
+                        tab->row[x][key + 32 * e] = r[e];
+                        tab->ks[x][key + 32 * e] = (uint8_t)k[e];
+                        tab->vs[x][key + 32 * e] = (uint8_t)v[e];
+                    }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh->tab_full[x]);
                 }
@@ -672,7 +708,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
         }
     } else if (warp < 8) {
         // ---------------- softmax and epilogue ----------------
-        constexpr int kPart = kTcKeys / 2;
+        constexpr int kPart = 64;  // a tile's keys, or half of them
         const int quad = warp & 3, rl = quad * 32 + lane, r = (int)rank * 128 + rl;
         const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
         const float c2 = a.scale * 1.4426950408889634f;
@@ -687,13 +723,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
             const int t = it.t0 + r / kGrp;  // this row's position (rows past the tokens: not written)
             float m = -INFINITY, l = 0.f;          // running maximum of c2 s, sum of exp2(c2 s - m)
             for (int i = it.i0; i < it.i1; ++i, ++T) {
-                const uint32_t buf = T & 1, s_addr = lane_addr + buf * kTcKeys;
+                const uint32_t buf = T & 1, s_addr = lane_addr + buf * kKeys;
                 if (!await(&sh->s_full[buf], (T >> 1) & 1)) break;
                 const int j0 = it.tile(i);
                 // unless every row sees every key of the tile: columns hi and below, from lo on or below sk
-                const bool edge = !(j0 + kTcKeys - 1 <= it.t0 &&
-                                    (a.window <= 0 || it.t_last - j0 < a.window || j0 + kTcKeys <= a.sinks));
-                int hi = kTcKeys, lo = 0, sk = 0;
+                const bool edge = !(j0 + kKeys - 1 <= it.t0 &&
+                                    (a.window <= 0 || it.t_last - j0 < a.window || j0 + kKeys <= a.sinks));
+                int hi = kKeys, lo = 0, sk = 0;
                 if (edge) {
                     hi = t - j0;
                     lo = a.window > 0 && a.window <= hi ? hi - (int)a.window + 1 : 0;
@@ -728,12 +764,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                 // there is room for the first half only, and the second is read again below.
                 float s0[kPart], s1[kPart];
                 float mx = -INFINITY;
-                load(1, s1);
-                if (!kFp8) load(0, s0);
-                tmem_wait_ld();
-                mask(1, s1);
-                mx = largest(mx, s1);
-                if (kFp8) {
+                if (kCtas == 2) {
+                    load(1, s1);
+                    if (!kFp8) load(0, s0);
+                    tmem_wait_ld();
+                    mask(1, s1);
+                    mx = largest(mx, s1);
+                }
+                if (kFp8 || kCtas == 1) {
                     load(0, s0);
                     tmem_wait_ld();
                 }
@@ -782,12 +820,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                     }
                 };
                 probabilities(0, s0);
-                if (kFp8) {
-                    load(1, s0);
-                    tmem_wait_ld();
-                    mask(1, s0);
+                if (kCtas == 2) {
+                    if (kFp8) {
+                        load(1, s0);
+                        tmem_wait_ld();
+                        mask(1, s0);
+                    }
+                    probabilities(1, kFp8 ? s0 : s1);
                 }
-                probabilities(1, kFp8 ? s0 : s1);
                 const float2 la = unpack2(add2(l01, l23));
                 l = la.x + la.y;
                 tmem_wait_st();
@@ -798,7 +838,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
             // O of the whole item
             if (!ok || !await(&sh->o_full, n & 1)) break;
             ++n;
-            const bool mine = r / kGrp < it.nq && r < kTcRows, none = l == 0.f;
+            const bool mine = r / kGrp < it.nq && r < C::kRows, none = l == 0.f;
             const float inv = none ? 0.f : 1.f / l;
             const bool complete = it.i0 == 0 && it.i1 == it.nt;
             const int64_t piece = 2 * worker + (it.i0 == 0 ? 1 : 0);
@@ -829,7 +869,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                     for (int j = 0; j < 4; ++j)
                         if (j < rows) *reinterpret_cast<uint4 *>(dst + j * kD) = v[j];
                 } else {
-                    float *dst = a.ws + (piece * kTcRows + r4) * kD + c * 32 + q * 4;
+                    float *dst = a.ws + (piece * C::kRows + r4) * kD + c * 32 + q * 4;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint4 v[4];
@@ -849,22 +889,22 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
             if (lane == 0) arrive_leader_relaxed(&sh->o_empty);
             if (mine) {
                 const float lse2 = none ? -INFINITY : m + log2f(l);
-                if (!complete) a.ws[2 * workers * kTcRows * kD + piece * kTcRows + r] = lse2;
+                if (!complete) a.ws[2 * workers * C::kRows * kD + piece * C::kRows + r] = lse2;
                 else if (a.lse != nullptr) a.lse[row] = lse2 * 0.6931471805599453f;
             }
         }
     } else if (kFp8) {
         // ---------------- e4m3 codes to bf16 ----------------
-        const TcTable *tab = reinterpret_cast<const TcTable *>(smem + C::kOffTable);
+        const TcTable<kCtas> *tab = reinterpret_cast<const TcTable<kCtas> *>(smem + C::kOffTable);
         const int cw = warp - 8, k8 = lane >> 2, piece = lane & 3;
         const uint32_t ring_u = smem_u32(ring);
         const uint8_t *kp = static_cast<const uint8_t *>(a.pool.k) + piece * 16;
         const uint8_t *vp = static_cast<const uint8_t *>(a.pool.v) + rank * 128 + piece * 16;
         uint32_t stage = 0, ph = 1, n = 0;
-        // A warp converts 8 keys of K (all dims) and 16 of V (this CTA's dims) per tile; the next
+        // A warp converts 8 keys of K (all dims) and 8 or, in a pair, 16 of V (this CTA's dims) per tile; the next
         // half tile of the other kind is loaded before one is converted.
         uint4 kreg[4], vreg[4];
-        uint32_t kb, vb[2];
+        uint32_t kb, vb[kCtas];
         auto load_k = [&](uint32_t x) {
             const int key = (int)rank * 64 + cw * 8 + k8;
             const int32_t row = tab->row[x][key];
@@ -876,14 +916,14 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
         };
         auto load_v = [&](uint32_t x) {
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int key = cw * 16 + q * 8 + k8;
+            for (int q = 0; q < kCtas; ++q) {
+                const int key = (cw * kCtas + q) * 8 + k8;
                 const int32_t row = tab->row[x][key];
                 vb[q] = tab->vs[x][key];
                 const uint8_t *src = vp + (int64_t)row * kD;
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    vreg[q * 2 + c] = row >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
+                for (int c = 0; c < C::kVChunks; ++c)
+                    vreg[q * C::kVChunks + c] = row >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + c * 64)) : make_uint4(0u, 0u, 0u, 0u);
             }
         };
         auto table_ready = [&](uint32_t t) -> bool {
@@ -922,11 +962,11 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                 if (i > 0) {  // V(i - 1)
                     if (!slot_ready()) break;
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
+                    for (int q = 0; q < kCtas; ++q) {
                         const RowScale sc = row_scale(vb[q]);
-                        const uint32_t dst = ring_u + stage * kTcSlot + (cw * 16 + q * 8 + k8) * 128;
+                        const uint32_t dst = ring_u + stage * kTcSlot + ((cw * kCtas + q) * 8 + k8) * 128;
 #pragma unroll
-                        for (int c = 0; c < 2; ++c) codes_to_slot(vreg[q * 2 + c], sc, dst + c * kTcVChunk, 2 * piece, k8);
+                        for (int c = 0; c < C::kVChunks; ++c) codes_to_slot(vreg[q * C::kVChunks + c], sc, dst + c * C::kVChunk, 2 * piece, k8);
                     }
                     slot_done();
                 }
@@ -942,10 +982,13 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
 
     tc_fence_before();
     __syncthreads();
-    cluster_sync();  // no arrival of the peer is under way
+    if (kCtas == 2) cluster_sync();  // no arrival of the peer is under way
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcCols) : "memory");
+        if (kCtas == 1)
+            tmem_dealloc(tmem, kTcCols);
+        else
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcCols) : "memory");
     }
 }
 
@@ -965,8 +1008,8 @@ cudaError_t tc_workers(int64_t *out)
     }
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(2 * kTcMaxPairs);
-    cfg.blockDim = dim3(TcCfg<kFp8>::kThreads);
-    cfg.dynamicSmemBytes = TcCfg<kFp8>::kSmem;
+    cfg.blockDim = dim3(TcCfg<kFp8, 2>::kThreads);
+    cfg.dynamicSmemBytes = TcCfg<kFp8, 2>::kSmem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -974,7 +1017,7 @@ cudaError_t tc_workers(int64_t *out)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, chunk_tc_kernel<kFp8>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, chunk_tc_kernel<kFp8, 2>, &cfg);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorInvalidConfiguration;
     if (n > kTcMaxPairs) n = (int)kTcMaxPairs;
@@ -983,37 +1026,46 @@ cudaError_t tc_workers(int64_t *out)
     return cudaSuccess;
 }
 
-size_t tc_prefix_offset() { return (size_t)(2 * kTcMaxPairs) * kTcRows * (kD + 1) * sizeof(float); }
+size_t tc_prefix_offset()
+{
+    static_assert(kTcMaxPairs * 252 >= kTcMaxSingles * 120, "the pairs' pieces are the larger ones");
+    return (size_t)(2 * kTcMaxPairs) * 252 * (kD + 1) * sizeof(float);
+}
 
-template <bool kFp8>
+template <bool kFp8, int kCtas>
 cudaError_t launch_tc(const ChunkArgs &a, cudaStream_t stream)
 {
+    using C = TcCfg<kFp8, kCtas>;
     CUtensorMap mq, mq4;  // ten tokens, and four heads of one, of 64 dims
     if (!make_tmap_3d(&mq, a.q, kD, kHQ, (uint64_t)a.total_q, kD * 2, (uint64_t)kHQ * kD * 2, 64, kGrp, 10) ||
         !make_tmap_3d(&mq4, a.q, kD, kHQ, (uint64_t)a.total_q, kD * 2, (uint64_t)kHQ * kD * 2, 64, 4, 1))
         return cudaErrorInvalidValue;
-    cudaError_t e = set_smem_attr_once(reinterpret_cast<const void *>(chunk_tc_kernel<kFp8>), TcCfg<kFp8>::kSmem);
+    cudaError_t e = set_smem_attr_once(reinterpret_cast<const void *>(chunk_tc_kernel<kFp8, kCtas>), C::kSmem);
     if (e != cudaSuccess) return e;
-    int64_t workers = 0;
-    e = tc_workers<kFp8>(&workers);
-    if (e != cudaSuccess) return e;
+    int64_t workers = num_sms();
+    if (workers > kTcMaxSingles) workers = kTcMaxSingles;
+    if (kCtas == 2) {
+        e = tc_workers<kFp8>(&workers);
+        if (e != cudaSuccess) return e;
+    }
     int64_t *prefix = reinterpret_cast<int64_t *>(reinterpret_cast<uint8_t *>(a.ws) + tc_prefix_offset());
-    e = launch_pdl(chunk_tc_kernel<kFp8>, dim3((unsigned)(2 * workers)), dim3(TcCfg<kFp8>::kThreads), TcCfg<kFp8>::kSmem,
-                   stream, mq, mq4, a, prefix);
+    e = launch_pdl(chunk_tc_kernel<kFp8, kCtas>, dim3((unsigned)(kCtas * workers)), dim3(C::kThreads), C::kSmem, stream, mq,
+                   mq4, a, prefix);
     if (e != cudaSuccess) return e;
-    return launch_chunk_merge<kTcTok, kTcKeys>(a, prefix, workers, stream);
+    return launch_chunk_merge<C::kTok, C::kKeys>(a, prefix, workers, stream);
 }
 
 }  // namespace
 
 size_t chunk_tc_workspace_bytes(int batch, int64_t total_q)
 {
-    return tc_prefix_offset() + (size_t)(chunk_slots<kTcTok>(total_q, batch) + 1) * sizeof(int64_t);
+    return tc_prefix_offset() + (size_t)(chunk_slots<10>(total_q, batch) + 1) * sizeof(int64_t);
 }
 
 cudaError_t launch_chunk_tc(const ChunkArgs &a, cudaStream_t stream)
 {
-    return a.pool.fp8 ? launch_tc<true>(a, stream) : launch_tc<false>(a, stream);
+    if (a.max_len_q <= 10) return a.pool.fp8 ? launch_tc<true, 1>(a, stream) : launch_tc<false, 1>(a, stream);
+    return a.pool.fp8 ? launch_tc<true, 2>(a, stream) : launch_tc<false, 2>(a, stream);
 }
 
 }  // namespace qsa

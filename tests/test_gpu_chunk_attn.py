@@ -35,7 +35,7 @@ LENGTHS = [
     (16, [1], [1]), (64, [1], [8191]), (1, [1, 1], [5, 130]), (12, [1] * 9, [1, 2, 63, 64, 65, 127, 128, 129, 700]),
     (64, [1] * 40, [100 + 37 * i for i in range(40)]),
     (16, [4, 3, 2, 1], [4, 300, 129, 1000]), (8, [0, 4, 0, 5, 0], [10, 300, 0, 5, 0]),
-    (32, [21, 22, 43], [21, 150, 43]), (7, [10, 11, 64, 65], [300, 11, 64, 201]),
+    (32, [21, 22, 43], [21, 150, 43]), (16, [10, 9, 1], [300, 9, 1000]), (48, [8] * 5, [8, 64, 65, 4000, 129]), (7, [10, 11, 64, 65], [300, 11, 64, 201]),
     (128, [701], [701]), (16, [128, 1, 300], [900, 2000, 300]), (64, [0, 0], [0, 5]), (5, [257], [2049]),
 ]
 
