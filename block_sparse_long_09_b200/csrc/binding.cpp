@@ -246,7 +246,7 @@ PyObject *chunk_attn_paged(PyObject *, PyObject *const *a, Py_ssize_t n)
         check_device(q, {&p.k, &p.v, &p.ks, &p.vs, &p.table, &cu_q, &cu_k, &o, &lse, &ws});
         const qsa_config *cfg = config(a[0]);
         if (!o.defined()) o = empty(q.sizes(), at::kBFloat16, q);
-        if (!lse.defined() && a[15] == Py_True) lse = empty({q.size(0), kHQ}, at::kFloat, q);
+        if (!lse.defined() && PyObject_IsTrue(a[15]) == 1) lse = empty({q.size(0), kHQ}, at::kFloat, q);
         if (!ws.defined())
             ws = empty({(int64_t)api.workspace(cfg, QSA_OP_CHUNK_PAGED, (int32_t)batch, q.size(0), max_k)}, at::kByte, q);
         const long st = api.chunk(cfg, ptr<qsa_bf16>(q), p.format, ptr<void>(p.k), ptr<void>(p.v), ptr<uint8_t>(p.ks),

@@ -536,18 +536,21 @@ qsa_status qsa_cache_read_paged(const qsa_config *cfg, int32_t format, const voi
  * few first tokens that stay visible); window = 0: no window, sinks is ignored.
  *   q    [total_q, n_heads_q, head_dim] bf16, 16-byte aligned, and so o
  *   lse  [total_q, n_heads_q] fp32 natural log-sum-exp of the scaled logits, or NULL
- *   max_len_q host: a bound of every L_q,s (chooses the kernel; the result does not depend
- *        on it beyond rounding)
+ *   max_len_q host: a bound of every L_q,s (chooses the kernel; a wrong one costs time, and the
+ *        result does not depend on it beyond rounding)
+ *   o must not overlap q or the pool, nor lse the pool
  * fp32 softmax and accumulation, probabilities and output rounded to bf16.  E4M3 codes enter
  * the products unrounded.  A row without a visible key (a negative position, an empty cache)
  * gets o = 0, lse = -inf.  Cache memory at positions behind a sequence's end and pages wholly
  * outside the window are not read into any result and may hold anything; their table
  * entries are not looked up.  A visible position without a page counts as a zero key and
- * value and flags QSA_ERR_DEVICE_CHECK.  In a BF16 pool a non-finite V value may reach rows of
- * neighbouring tokens that do not see it.
- * Workspace: qsa_workspace_size(cfg, QSA_OP_CHUNK_PAGED, batch, total_q, 0) bytes, 16-byte
- * aligned; calls that may overlap on the GPU need one each.  No attention between two calls
- * is kept in it.
+ * value and flags QSA_ERR_DEVICE_CHECK.  Several new tokens of a sequence: a non-finite V value that one
+ * of them sees may make a NaN of another's output too, though that one does not see it.
+ * (e4m3 pages and max_len_q <= 1: q and the probabilities as fp16 relative to their row's largest,
+ * the probabilities' rounding 2^-12; otherwise probabilities as bf16.)
+ * Workspace: qsa_workspace_size(cfg, QSA_OP_CHUNK_PAGED, batch, total_q, 0) bytes (about 41 MB), 16-byte
+ * aligned; calls that may overlap on the GPU need one each.  Nothing is kept in it from one call
+ * to the next, and it may hold anything before.
  */
 qsa_status qsa_chunk_attn_paged(const qsa_config *cfg, const qsa_bf16 *q, int32_t format, const void *k_pages,
                                 const void *v_pages, const uint8_t *k_scales, const uint8_t *v_scales,

@@ -287,6 +287,22 @@ def test_offsets_past_32_bits(qsa, fp8):
     assert qsa.device_status(clear=True) == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("most", [1, 5, 30])
+def test_large_batches(qsa, most, fp8):
+    """More sequences than the kernels keep the lengths of at hand, some of them empty."""
+    g = torch.Generator().manual_seed(most)
+    lens_q = torch.randint(0, most + 1, (200,), generator=g).tolist()
+    lens_q[7] = most
+    lens_k = [n + int(x) for n, x in zip(lens_q, torch.randint(0, 400, (200,), generator=g))]
+    pool = Pool(lens_k, 16, fp8, seed=most).fill()
+    q = queries(sum(lens_q))
+    for window, sinks in ((0, 0), (60, 4)):
+        o, lse = attend(qsa, q, pool, lens_q, window, sinks)
+        check_attend(q, pool, lens_q, o, lse, window, sinks)
+    assert qsa.device_status(clear=True) == 0
+
+
 def test_equals_the_packed_dense_attention(qsa):
     """A whole prompt at once: the packed dense kernel computes the same."""
     lens = [300, 129]
