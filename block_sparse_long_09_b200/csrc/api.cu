@@ -741,7 +741,7 @@ qsa_status qsa_chunk_attn_paged(const qsa_config *cfg, const qsa_bf16 *q, int32_
     st = check_pool(cfg, format, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, block_table, max_pages);
     if (st != QSA_OK) return st;
     if (total_q == 0) return QSA_OK;
-    if (total_q >= ((int64_t)1 << 28)) return QSA_ERR_UNSUPPORTED;
+    if (total_q >= ((int64_t)1 << 28) || batch >= (1 << 28)) return QSA_ERR_UNSUPPORTED;
     if (q == nullptr || o == nullptr || !al16(q) || !al16(o)) return QSA_ERR_INVALID_ARG;
     if (ws == nullptr || ws_bytes < chunk_workspace_bytes(batch, total_q)) return QSA_ERR_WORKSPACE_TOO_SMALL;
     if (!al16(ws)) return QSA_ERR_INVALID_ARG;

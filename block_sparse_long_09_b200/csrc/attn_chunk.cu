@@ -38,6 +38,7 @@ namespace qsa {
 namespace {
 
 constexpr int kDecWarps = 8, kDecThreads = kDecWarps * 32, kDecKeys = 16 * kDecWarps;
+constexpr int kDecRestart = 2;  // tiles that another item on a worker costs (5 us, a tile 2.5)
 
 template <bool kFp8>
 struct DecCfg {
@@ -116,12 +117,12 @@ __device__ __forceinline__ float dec_ex2(float x)
 
 template <bool kFp8>
 __global__ void __launch_bounds__(kDecThreads, 1)
-chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
+chunk_decode_kernel(const ChunkArgs a, int2 *__restrict__ pieces)
 {
     using C = DecCfg<kFp8>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ ChunkShare share;
-    __shared__ int64_t scan[kDecWarps];
+    __shared__ int64_t scan[2 * kDecWarps];
     __shared__ ChunkLengths lengths;
     pdl_enter();
     lengths.fill(a);
@@ -131,9 +132,10 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
     float *stats = reinterpret_cast<float *>(smem + C::kOffStats);  // [maximum, sum][warp][16 rows]
     float *states = reinterpret_cast<float *>(smem + C::kOffRing);  // [warp][12 rows][kMergePitch], at an item's end
     const uint32_t ring = smem_u32(smem + C::kOffRing) + warp * C::kRing * C::kSlot;
-    chunk_share<1, kDecKeys, kDecThreads>(a, blockIdx.x, gridDim.x, &share, scan, blockIdx.x == 0 ? prefix : nullptr,
-                                              &lengths);
-    int64_t at = share.ts, slot = share.slot, first = share.first;
+    chunk_share<1, kDecKeys, kDecThreads, kDecRestart>(a, blockIdx.x, gridDim.x, &share, scan,
+                                                       blockIdx.x == 0 ? pieces : nullptr, &lengths);
+    int64_t at = share.ts, first = share.first;
+    int slot = share.slot;
     const int64_t te = share.te;
     const float c2 = a.scale * 1.4426950408889634f;
 
@@ -146,9 +148,9 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
         const int hd = at >= first + g.nt ? 1 : 0;  // KV head
         const int64_t item = first + (int64_t)hd * g.nt;
         const int i0 = (int)(at - item), i1 = te - item < g.nt ? (int)(te - item) : g.nt;
-        const int t = (int)g.t0, ns = g.ns, w_tile = (int)g.w_tile;
+        const int t = g.t0, ns = g.ns, w_tile = g.w_tile;
         const int near = a.window > 0 && a.window <= t ? t - (int)a.window + 1 : 0, sinks = (int)a.sinks;
-        const int64_t row_q = g.row0 * kHQ + hd * kGrp;
+        const int64_t row_q = (int64_t)g.row0 * kHQ + hd * kGrp;
         const int32_t *table = a.pool.table + (int64_t)g.s * a.pool.max_pages;
         auto sees = [&](int j) -> bool { return j <= t && (j >= near || j < sinks); };
         auto tile = [&](int i) -> int { return (i < ns ? i : w_tile + (i - ns)) * kDecKeys + warp * 16; };
@@ -523,27 +525,27 @@ chunk_decode_kernel(const ChunkArgs a, int64_t *__restrict__ prefix)
 
 constexpr int64_t kMaxWorkers = 160;  // CTAs of the kernel, at most (the workspace's bound)
 
-size_t dec_prefix_offset() { return (size_t)(2 * kMaxWorkers) * kGrp * (kD + 1) * sizeof(float); }
+size_t dec_pieces_offset() { return (size_t)(2 * kMaxWorkers) * kGrp * (kD + 1) * sizeof(float); }
 
 template <bool kFp8>
 cudaError_t launch_decode(const ChunkArgs &a, cudaStream_t stream)
 {
-    int64_t *prefix = reinterpret_cast<int64_t *>(reinterpret_cast<uint8_t *>(a.ws) + dec_prefix_offset());
+    int2 *pieces = reinterpret_cast<int2 *>(reinterpret_cast<uint8_t *>(a.ws) + dec_pieces_offset());
     int64_t workers = num_sms();
     if (workers > kMaxWorkers) workers = kMaxWorkers;
     cudaError_t e = set_smem_attr_once(reinterpret_cast<const void *>(chunk_decode_kernel<kFp8>), DecCfg<kFp8>::kSmem);
     if (e != cudaSuccess) return e;
     e = launch_pdl(chunk_decode_kernel<kFp8>, dim3((unsigned)workers), dim3(kDecThreads), DecCfg<kFp8>::kSmem, stream, a,
-                   prefix);
+                   pieces);
     if (e != cudaSuccess) return e;
-    return launch_chunk_merge<1, kDecKeys>(a, prefix, workers, stream);
+    return launch_chunk_merge<1, kDecKeys, kDecRestart>(a, pieces, workers, stream);
 }
 
 }  // namespace
 
 size_t chunk_workspace_bytes(int batch, int64_t total_q)
 {
-    const size_t own = dec_prefix_offset() + (size_t)(chunk_slots<1>(total_q, batch) + 1) * sizeof(int64_t);
+    const size_t own = dec_pieces_offset() + (size_t)chunk_slots<1>(total_q, batch) * 2 * sizeof(int2);
     const size_t tc = chunk_tc_workspace_bytes(batch, total_q);
     return own > tc ? own : tc;
 }

@@ -57,7 +57,7 @@ struct TcShared {
     uint64_t tab_full[kTcTables], tab_empty[kTcTables];
     uint32_t tmem_base;
     int abort_flag;
-    int64_t scan[16], walk[16][3];
+    int64_t scan[32], walk[16][3];
     ChunkShare share;
     ChunkLengths lengths;
 };
@@ -71,6 +71,7 @@ struct TcTable {  // e4m3: pool rows (of the KV head, -1: none) and scale bytes 
 template <bool kFp8, int kCtas>
 struct TcCfg {
     static constexpr int kTok = kCtas == 2 ? 21 : 10, kRows = kTok * kGrp, kKeys = 64 * kCtas;
+    static constexpr int kRestart = kCtas == 2 ? 8 : 16;  // tiles that another item on a worker costs (11 us)
     static constexpr int kVChunks = 4 / kCtas, kVChunk = kKeys * 128;  // 64 dims of a V tile
     static constexpr int kThreads = kFp8 ? 512 : 256;
     static constexpr int kStages = kFp8 ? 4 : 5;
@@ -308,7 +309,8 @@ struct TcWalk {
     // by one lane or by all lanes of the warp together
     __device__ __forceinline__ bool next(const ChunkArgs &a)
     {
-        int64_t at = state[0], slot = state[1], first = state[2];
+        int64_t at = state[0], first = state[2];
+        int slot = (int)state[1];
         const int64_t te = sh->share.te;
         if (at >= te) return false;
         ChunkGroup g = chunk_group<kTok, kKeys>(a, slot, &sh->lengths);
@@ -324,9 +326,9 @@ struct TcWalk {
         nq = g.nq;
         nt = g.nt;
         ns = g.ns;
-        w_tile = (int)g.w_tile;
-        row0 = (int)g.row0;
-        t0 = (int)g.t0;
+        w_tile = g.w_tile;
+        row0 = g.row0;
+        t0 = g.t0;
         t_first = t0 > 0 ? t0 : 0;
         t_last = t0 + nq - 1;
         near = a.window > 0 ? t_first - (int)a.window + 1 : 0;
@@ -422,7 +424,7 @@ __device__ __forceinline__ void codes_to_slot(const uint4 &codes, const RowScale
 template <bool kFp8, int kCtas>
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__((TcCfg<kFp8, kCtas>::kThreads), 1)
 chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_q4,
-                const ChunkArgs a, int64_t *__restrict__ prefix)
+                const ChunkArgs a, int2 *__restrict__ pieces)
 {
     using C = TcCfg<kFp8, kCtas>;
     constexpr int kKeys = C::kKeys;
@@ -468,8 +470,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
         }
     }
     sh->lengths.fill(a);
-    chunk_share<C::kTok, kKeys, C::kThreads>(a, worker, workers, &sh->share, sh->scan,
-                                              blockIdx.x == 0 ? prefix : nullptr, &sh->lengths);
+    chunk_share<C::kTok, kKeys, C::kThreads, C::kRestart>(a, worker, workers, &sh->share, sh->scan,
+                                                          blockIdx.x == 0 ? pieces : nullptr, &sh->lengths);
     tc_fence_before();
     __syncthreads();
     if (kCtas == 2) cluster_sync();  // both CTAs' barriers are initialised
@@ -1034,7 +1036,7 @@ cudaError_t tc_workers(int64_t *out)
     return cudaSuccess;
 }
 
-size_t tc_prefix_offset()
+size_t tc_pieces_offset()
 {
     static_assert(kTcMaxPairs * 252 >= kTcMaxSingles * 120, "the pairs' pieces are the larger ones");
     return (size_t)(2 * kTcMaxPairs) * 252 * (kD + 1) * sizeof(float);
@@ -1056,18 +1058,18 @@ cudaError_t launch_tc(const ChunkArgs &a, cudaStream_t stream)
         e = tc_workers<kFp8>(&workers);
         if (e != cudaSuccess) return e;
     }
-    int64_t *prefix = reinterpret_cast<int64_t *>(reinterpret_cast<uint8_t *>(a.ws) + tc_prefix_offset());
+    int2 *pieces = reinterpret_cast<int2 *>(reinterpret_cast<uint8_t *>(a.ws) + tc_pieces_offset());
     e = launch_pdl(chunk_tc_kernel<kFp8, kCtas>, dim3((unsigned)(kCtas * workers)), dim3(C::kThreads), C::kSmem, stream, mq,
-                   mq4, a, prefix);
+                   mq4, a, pieces);
     if (e != cudaSuccess) return e;
-    return launch_chunk_merge<C::kTok, C::kKeys>(a, prefix, workers, stream);
+    return launch_chunk_merge<C::kTok, C::kKeys, C::kRestart>(a, pieces, workers, stream);
 }
 
 }  // namespace
 
 size_t chunk_tc_workspace_bytes(int batch, int64_t total_q)
 {
-    return tc_prefix_offset() + (size_t)(chunk_slots<10>(total_q, batch) + 1) * sizeof(int64_t);
+    return tc_pieces_offset() + (size_t)chunk_slots<10>(total_q, batch) * 2 * sizeof(int2);
 }
 
 // the single CTA's kernel where all groups are small (see above)

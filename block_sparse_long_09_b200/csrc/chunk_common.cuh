@@ -9,13 +9,17 @@
 //
 // A group's visible keys are [0, min(sinks, w0)) and [w0, t_last], w0 = the first position
 // inside its first token's window, cut into tiles of kKeys aligned at multiples of kKeys.
-// The tiles of all items, in item order, are cut into equal shares, one per worker (a
-// CTA or a CTA pair), from the lengths on the device alone: a batch of any mix of lengths is
-// balanced and a captured launch stays valid as the caches grow.  An item inside one share
-// is finished there.  A cut item is attended in pieces whose normalised outputs and
-// log-sum-exps (base 2) the merge kernel adds up: the piece that begins the item goes to
-// slot 2 c + 1 of its share c, any later piece to slot 2 c (a share has at most one of
-// each).
+// The tiles are shared out to the workers (a CTA or a CTA pair) from the lengths on the device
+// alone: a batch of any mix of lengths is balanced and a captured launch stays valid as
+// the caches grow.  Two ways:
+//   even    the tiles of all items, in item order, in equal shares; a share may end one item and
+//           begin another (a restart costs as much as kRestart tiles: its loads, Q and the epilogue)
+//   apart   no more than one item per worker, workers dealt to the items by their tiles: less even, for
+//           batches whose shares are a few tiles
+// An item that one worker has whole is finished there.  A cut item is attended in pieces whose
+// normalised outputs and log-sum-exps (base 2) the merge kernel adds up: the piece that begins the
+// item goes to slot 2 c + 1 of its worker c, any later piece to slot 2 c (a worker has at
+// most one of each).
 #pragma once
 #include "kernels.cuh"
 
@@ -28,18 +32,12 @@ constexpr int kHQ = 24, kHKV = 2, kD = 256, kGrp = kHQ / kHKV;
 struct ChunkGroup {
     int s;            // sequence
     int nq;           // tokens, 0: an empty slot
-    int64_t row0;     // first packed query row
-    int64_t t0;       // position of the first token (may be negative: no visible key)
+    int row0;         // first packed query row
+    int t0;           // position of the first token (may be negative: no visible key)
     int nt;           // key tiles
     int ns;           // leading tiles that hold the first tokens (sinks)
-    int64_t w_tile;   // tile index (of kKeys) of the first window tile
+    int w_tile;       // tile index (of kKeys) of the first window tile
 };
-
-// first key tile after the sinks, etc.: tile i of the group starts at position
-__device__ __forceinline__ int64_t tile_start(const ChunkGroup &g, int i, int keys)
-{
-    return (i < g.ns ? (int64_t)i : g.w_tile + (i - g.ns)) * keys;
-}
 
 // A batch's lengths in shared memory (up to kCuBatch sequences), for the searches of every role and item.
 constexpr int kCuBatch = 128;
@@ -57,43 +55,43 @@ struct ChunkLengths {
     }
 };
 
+// (lengths and positions are int32, rows fewer than 2^28, sequences fewer than 2^28)
 template <int kTok, int kKeys>
-__device__ __forceinline__ ChunkGroup chunk_group(const ChunkArgs &a, int64_t slot, const ChunkLengths *sh = nullptr)
+__device__ __forceinline__ ChunkGroup chunk_group(const ChunkArgs &a, int slot, const ChunkLengths *sh = nullptr)
 {
     const bool local = sh != nullptr && a.batch <= kCuBatch;
-    auto cu_q = [&](int i) -> int32_t { return local ? sh->q[i] : __ldg(a.cu_q + i); };
-    auto cu_k = [&](int i) -> int32_t { return local ? sh->k[i] : __ldg(a.cu_k + i); };
+    auto cu_q = [&](int i) -> int { return local ? sh->q[i] : __ldg(a.cu_q + i); };
+    auto cu_k = [&](int i) -> int { return local ? sh->k[i] : __ldg(a.cu_k + i); };
     ChunkGroup g;
     g.nt = g.ns = g.nq = 0;
     g.w_tile = g.row0 = g.t0 = 0;
     int lo = 0, hi = a.batch;  // the last s whose first slot is <= slot
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if ((int64_t)(cu_q(mid) / kTok) + mid <= slot) lo = mid; else hi = mid;
+        if (cu_q(mid) / kTok + mid <= slot) lo = mid; else hi = mid;
     }
     g.s = lo;
-    const int64_t q0 = cu_q(lo), q1 = cu_q(lo + 1);
-    const int64_t first = (slot - (q0 / kTok + lo)) * kTok, Lq = q1 - q0;
+    const int q0 = cu_q(lo), q1 = cu_q(lo + 1);
+    const int first = (slot - (q0 / kTok + lo)) * kTok, Lq = q1 - q0;
     if (q0 < 0 || first < 0 || first >= Lq) return g;
     if (q1 > a.total_q) {  // lengths that the query tensor does not hold
         set_device_status(QSA_ERR_DEVICE_CHECK);
         return g;
     }
-    const int64_t Lk = (int64_t)cu_k(lo + 1) - cu_k(lo);
-    g.nq = (int)(Lq - first < kTok ? Lq - first : kTok);
+    g.nq = Lq - first < kTok ? Lq - first : kTok;
     g.row0 = q0 + first;
-    g.t0 = Lk - Lq + first;
-    const int64_t last = g.t0 + g.nq - 1;
+    g.t0 = cu_k(lo + 1) - cu_k(lo) - Lq + first;
+    const int last = g.t0 + g.nq - 1;
     if (last < 0) return g;
-    const int64_t t_first = g.t0 > 0 ? g.t0 : 0;
-    const int64_t w0 = a.window > 0 && t_first - a.window + 1 > 0 ? t_first - a.window + 1 : 0;
-    const int64_t sinks = a.sinks < w0 ? a.sinks : w0;
-    const int64_t end = last / kKeys + 1;
-    int64_t ns = (sinks + kKeys - 1) / kKeys, w = w0 / kKeys;
+    const int t_first = g.t0 > 0 ? g.t0 : 0;
+    const int w0 = a.window > 0 && t_first >= a.window ? t_first - (int)a.window + 1 : 0;
+    const int sinks = a.sinks < w0 ? (int)a.sinks : w0;
+    const int end = last / kKeys + 1;
+    int ns = sinks / kKeys + (sinks % kKeys != 0 ? 1 : 0), w = w0 / kKeys;
     if (ns >= w) ns = w = 0;  // the sinks reach the window's first tile: one range from 0
-    g.ns = (int)ns;
+    g.ns = ns;
     g.w_tile = w;
-    g.nt = (int)(ns + end - w);
+    g.nt = ns + end - w;
     return g;
 }
 
@@ -106,85 +104,146 @@ __host__ __device__ __forceinline__ int64_t chunk_slots(int64_t total_q, int bat
 
 struct ChunkShare {
     int64_t ts, te;       // this worker's tiles [ts, te) of the call's
-    int64_t slot, first;  // the group slot that holds ts and that slot's first tile
+    int64_t first;        // first tile of the group slot that holds ts
+    int slot;             // that slot
 };
 
-// first tile of share c
-__device__ __forceinline__ int64_t share_start(int64_t c, int64_t total, int64_t workers)
+// x / y of numbers that mostly fit 32 bits
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y)
 {
-    const int64_t x = c * total;
-    return x < ((int64_t)1 << 32) ? (int64_t)((uint32_t)x / (uint32_t)workers) : x / workers;
+    return (x | y) < ((int64_t)1 << 32) ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
-// This worker's share, by the whole CTA (threads a power of two of whole warps); `scan`: a
-// shared array of one entry per warp.  `prefix` (worker 0's CTA, or null): the first tile
-// of every slot and, behind them, the total, for the merge.
-template <int kTok, int kKeys, int kThreads>
-__device__ __forceinline__ void chunk_share(const ChunkArgs &a, int64_t worker, int64_t workers, ChunkShare *out,
-                                            int64_t *scan, int64_t *prefix, const ChunkLengths *sh)
+// first tile of share c (even)
+__device__ __forceinline__ int64_t share_start(int64_t c, int64_t total, int64_t workers) { return divide(c * total, workers); }
+
+struct ChunkTotals {
+    int64_t tiles, items;
+    bool apart;
+};
+template <int kRestart>
+__device__ __forceinline__ ChunkTotals chunk_totals(int64_t tiles, int64_t items, int64_t workers)
+{
+    return ChunkTotals{tiles, items, items <= workers && (tiles <= workers ||
+                       tiles * items < kRestart * workers * (workers - items))};
+}
+
+// workers of an item of nt tiles (apart): at most one per tile, all items' together at most `workers`
+__device__ __forceinline__ int item_workers(int nt, const ChunkTotals &t, int64_t workers)
+{
+    if (nt == 0) return 0;
+    const int64_t n = 1 + divide(nt * (workers - t.items), t.tiles);
+    return n < nt ? (int)n : nt;
+}
+
+// sums over the CTA's threads of x and y; before: over the threads before this one.  `scan`: two entries per warp
+template <int kThreads>
+__device__ __forceinline__ void block_scan(int64_t x, int64_t y, int64_t *scan, int64_t &x_before, int64_t &y_before,
+                                           int64_t &x_all, int64_t &y_all)
 {
     constexpr int kWarps = kThreads / 32;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t slots = chunk_slots<kTok>(a.total_q, a.batch);
-    const int64_t per = (slots + kThreads - 1) / kThreads;  // consecutive slots of a thread
-    const int64_t u0 = tid * per < slots ? tid * per : slots, u1 = u0 + per < slots ? u0 + per : slots;
-    int64_t mine = 0;
-    for (int64_t u = u0; u < u1; ++u) mine += kHKV * (int64_t)chunk_group<kTok, kKeys>(a, u, sh).nt;
-    int64_t incl = mine;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t xi = x, yi = y;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += y;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - mine, total = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += scan[w];
-        total += scan[w];
-    }
-    const int64_t ts = share_start(worker, total, workers), te = share_start(worker + 1, total, workers);
-    if (tid == 0) {
-        out->ts = ts;
-        out->te = te;
-        out->slot = slots;
-        out->first = total;
-    }
-    __syncthreads();
-    const bool holds = ts < te && before <= ts && ts < before + mine;
-    if (holds || prefix != nullptr) {
-        int64_t at = before;
-        for (int64_t u = u0; u < u1; ++u) {
-            const int64_t n = kHKV * (int64_t)chunk_group<kTok, kKeys>(a, u, sh).nt;
-            if (prefix != nullptr) prefix[u] = at;
-            if (holds && at <= ts && ts < at + n) {
-                out->slot = u;
-                out->first = at;
-            }
-            at += n;
+        const int64_t u = __shfl_up_sync(0xffffffffu, xi, off), v = __shfl_up_sync(0xffffffffu, yi, off);
+        if (lane >= off) {
+            xi += u;
+            yi += v;
         }
     }
-    if (prefix != nullptr && tid == 0) prefix[slots] = total;
-    __syncthreads();
-}
-
-// does position t see key j <= t
-__device__ __forceinline__ bool chunk_sees(int64_t t, int64_t j, int64_t window, int64_t sinks)
-{
-    return j <= t && (window <= 0 || t - j < window || j < sinks);
-}
-
-// the pool row of position j of sequence s, -1 (flagged) when the table has no valid page
-__device__ __forceinline__ int64_t chunk_pool_row(const CachePool &c, int64_t s, int64_t j)
-{
-    uint32_t off;
-    const uint32_t p = c.page_of((uint32_t)j, &off);
-    const int32_t page = p < (uint32_t)c.max_pages ? __ldg(c.table + s * c.max_pages + p) : -1;
-    if (page < 0 || page >= c.num_pages) {
-        set_device_status(QSA_ERR_DEVICE_CHECK);
-        return -1;
+    __syncthreads();  // an earlier scan has been read
+    if (lane == 31) {
+        scan[warp] = xi;
+        scan[kWarps + warp] = yi;
     }
-    return (int64_t)page * c.page_size + off;
+    __syncthreads();
+    x_before = xi - x;
+    y_before = yi - y;
+    x_all = y_all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) {
+            x_before += scan[w];
+            y_before += scan[kWarps + w];
+        }
+        x_all += scan[w];
+        y_all += scan[kWarps + w];
+    }
+}
+
+// This worker's share, by the whole CTA (whole warps); `scan`: two shared entries per warp.  `pieces`
+// (worker 0's CTA, or null): every item's first and last worker, for the merge; none: 0, -1.
+template <int kTok, int kKeys, int kThreads, int kRestart>
+__device__ __forceinline__ void chunk_share(const ChunkArgs &a, int64_t worker, int64_t workers, ChunkShare *out,
+                                            int64_t *scan, int2 *pieces, const ChunkLengths *sh)
+{
+    const int slots = (int)chunk_slots<kTok>(a.total_q, a.batch);
+    const int per = (slots + kThreads - 1) / kThreads;  // consecutive slots of a thread
+    const int u0 = (int)threadIdx.x * per < slots ? (int)threadIdx.x * per : slots, u1 = u0 + per < slots ? u0 + per : slots;
+    int64_t mine = 0, items = 0;
+    for (int u = u0; u < u1; ++u) {
+        const int nt = chunk_group<kTok, kKeys>(a, u, sh).nt;
+        mine += kHKV * (int64_t)nt;
+        items += nt > 0 ? kHKV : 0;
+    }
+    if (threadIdx.x == 0) out->ts = out->te = out->first = out->slot = 0;
+    int64_t before, items_before, total, all;
+    block_scan<kThreads>(mine, items, scan, before, items_before, total, all);
+    if (total == 0) {
+        if (pieces != nullptr)
+            for (int u = u0; u < u1; ++u) pieces[2 * u] = pieces[2 * u + 1] = make_int2(0, -1);
+        __syncthreads();
+        return;
+    }
+    const ChunkTotals t = chunk_totals<kRestart>(total, all, workers);
+    if (t.apart) {
+        int64_t wanted = 0, at_w, unused, all_w, unused_all;
+        for (int u = u0; u < u1; ++u) wanted += kHKV * item_workers(chunk_group<kTok, kKeys>(a, u, sh).nt, t, workers);
+        block_scan<kThreads>(wanted, 0, scan, at_w, unused, all_w, unused_all);
+        const bool holds = at_w <= worker && worker < at_w + wanted;
+        if (holds || pieces != nullptr) {
+            int64_t at = before;
+            for (int u = u0; u < u1; ++u) {
+                const int nt = chunk_group<kTok, kKeys>(a, u, sh).nt, n = item_workers(nt, t, workers);
+                if (pieces != nullptr) {
+                    pieces[2 * u] = make_int2((int)at_w, (int)at_w + n - 1);
+                    pieces[2 * u + 1] = make_int2((int)at_w + n, (int)at_w + 2 * n - 1);
+                }
+                if (at_w <= worker && worker < at_w + kHKV * n) {
+                    const int hd = worker - at_w >= n ? 1 : 0;
+                    const int64_t j = worker - at_w - hd * n;
+                    out->slot = u;
+                    out->first = at;
+                    out->ts = at + hd * (int64_t)nt + divide(j * nt, n);
+                    out->te = at + hd * (int64_t)nt + divide((j + 1) * nt, n);
+                }
+                at += kHKV * (int64_t)nt;
+                at_w += kHKV * n;
+            }
+        }
+    } else {
+        const int64_t ts = share_start(worker, total, workers), te = share_start(worker + 1, total, workers);
+        const bool holds = ts < te && before <= ts && ts < before + mine;
+        if (holds || pieces != nullptr) {
+            int64_t at = before;
+            for (int u = u0; u < u1; ++u) {
+                const int64_t nt = chunk_group<kTok, kKeys>(a, u, sh).nt;
+                if (pieces != nullptr)
+                    for (int hd = 0; hd < kHKV; ++hd)  // the shares that hold the item's first and last tile
+                        pieces[2 * u + hd] = nt == 0 ? make_int2(0, -1)
+                                                     : make_int2((int)divide((at + hd * nt + 1) * workers - 1, total),
+                                                                 (int)divide((at + hd * nt + nt) * workers - 1, total));
+                if (holds && at <= ts && ts < at + kHKV * nt) {
+                    out->slot = u;
+                    out->first = at;
+                    out->ts = ts;
+                    out->te = te;
+                }
+                at += kHKV * nt;
+            }
+        }
+    }
+    __syncthreads();
 }
 
 constexpr int kMergeWarps = 8, kMergeThreads = kMergeWarps * 32;
@@ -194,61 +253,57 @@ static_assert(kMergeThreads == kD, "a thread per dim");
 // rows: a CTA per row, its eight warps over the row's pieces.  Where the item's tiles lie is worked out
 // from the lengths while the attention kernel still runs (that one was scheduled after everything
 // before it had completed); only then the CTA waits for it.
-template <int kTok, int kKeys>
+template <int kTok, int kKeys, int kRestart>
 __global__ void __launch_bounds__(kMergeThreads)
 chunk_merge_kernel(const ChunkArgs a, int64_t workers)
 {
     constexpr int kRows = kTok * kGrp, kAhead = 4;
     __shared__ float part[kMergeWarps][kD + 2];
-    __shared__ int64_t sums[2][kMergeWarps];
+    __shared__ int64_t scan[2 * kMergeWarps];
     const int slot = blockIdx.x >> 1, slots = (int)chunk_slots<kTok>(a.total_q, a.batch);
     const int hd = blockIdx.x & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t before = 0, all = 0;
+    int64_t tiles = 0, items = 0, p0 = 0, unused, total, all, before;
     for (int u = threadIdx.x; u < slots; u += kMergeThreads) {
-        const int64_t n = 2 * (int64_t)chunk_group<kTok, kKeys>(a, u).nt;
-        all += n;
-        if (u < slot) before += n;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        all += __shfl_xor_sync(0xffffffffu, all, off);
-        before += __shfl_xor_sync(0xffffffffu, before, off);
-    }
-    if (lane == 0) {
-        sums[0][warp] = all;
-        sums[1][warp] = before;
+        const int64_t nt = chunk_group<kTok, kKeys>(a, u).nt;
+        tiles += kHKV * nt;
+        items += nt > 0 ? kHKV : 0;
+        if (u < slot) p0 += kHKV * nt;
     }
     const ChunkGroup g = chunk_group<kTok, kKeys>(a, slot);
-    __syncthreads();
-    int64_t total = 0, p0 = 0;
-#pragma unroll
-    for (int w = 0; w < kMergeWarps; ++w) {
-        total += sums[0][w];
-        p0 += sums[1][w];
-    }
-    const int64_t rs = p0 + hd * (int64_t)g.nt, re = rs + g.nt;
+    block_scan<kMergeThreads>(tiles, items, scan, unused, unused, total, all);
+    block_scan<kMergeThreads>(p0, 0, scan, unused, unused, before, unused);
     int64_t c0 = 0, last = -1;
-    const int rows = g.nq * kGrp;
-    bool mine = blockIdx.y < rows;
     if (g.nt > 0) {
-        c0 = ((rs + 1) * workers - 1) / total;                                // the share that holds the item's first tile
-        if (share_start(c0 + 1, total, workers) >= re) mine = false;          // finished by one worker
-        last = (re * workers - 1) / total;                                    // and its last one
+        const ChunkTotals t = chunk_totals<kRestart>(total, all, workers);
+        if (t.apart) {
+            int64_t wanted = 0, at_w;
+            for (int u = threadIdx.x; u < slot; u += kMergeThreads)
+                wanted += kHKV * item_workers(chunk_group<kTok, kKeys>(a, u).nt, t, workers);
+            block_scan<kMergeThreads>(wanted, 0, scan, unused, unused, at_w, unused);
+            const int n = item_workers(g.nt, t, workers);
+            c0 = at_w + hd * n;
+            last = c0 + n - 1;
+        } else {
+            const int64_t rs = before + hd * (int64_t)g.nt;
+            c0 = divide((rs + 1) * workers - 1, total);
+            last = divide((rs + g.nt) * workers - 1, total);
+        }
     }
+    const int rows = g.nq * kGrp;
     pdl_enter();
-    if (!mine) return;  // uniform for the CTA
+    if (blockIdx.y >= rows || (g.nt > 0 && last == c0)) return;  // uniform for the CTA; finished by one worker
     const float *lse = a.ws + 2 * workers * kRows * kD;
     for (int r = blockIdx.y; r < rows; r += gridDim.y) {
         float mx = -INFINITY, sum = 0.f, acc[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) acc[j] = 0.f;
-        // pieces: slot 2 c0 + 1, then slot 2 c of every share c > c0 that holds tiles of the item
+        // pieces: slot 2 c0 + 1, then slot 2 c of every worker c > c0 that holds tiles of the item
         for (int64_t cb = c0 + warp; cb <= last; cb += kMergeWarps * kAhead) {
             float w[kAhead], x[kAhead][8];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 const int64_t c = cb + u * kMergeWarps;
-                const bool have = c <= last && (c == c0 || share_start(c + 1, total, workers) > share_start(c, total, workers));
+                const bool have = c <= last;
                 const int64_t p = c == c0 ? 2 * c0 + 1 : 2 * c;
                 w[u] = -INFINITY;
 #pragma unroll
@@ -304,25 +359,19 @@ chunk_merge_kernel(const ChunkArgs a, int64_t workers)
     }
 }
 
-// The same for many rows and few pieces each: a warp per kPer rows, with the tiles' prefix that the
-// attention kernel leaves.
+// The same for many rows and few pieces each: a warp per kPer rows, with the items' workers as the
+// attention kernel leaves them.
 template <int kTok, int kKeys, int kPer>
 __global__ void __launch_bounds__(kMergeThreads)
-chunk_merge_many_kernel(const ChunkArgs a, const int64_t *__restrict__ prefix, int64_t workers)
+chunk_merge_many_kernel(const ChunkArgs a, const int2 *__restrict__ pieces, int64_t workers)
 {
     constexpr int kRows = kTok * kGrp;
     pdl_enter();
-    const int64_t slot = blockIdx.x >> 1;
+    const int slot = blockIdx.x >> 1;
     const int hd = blockIdx.x & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t slots = chunk_slots<kTok>(a.total_q, a.batch);
-    const int64_t total = prefix[slots], p0 = prefix[slot], p1 = prefix[slot + 1];
-    const int64_t nt = (p1 - p0) >> 1, rs = p0 + hd * nt, re = rs + nt;
-    int64_t c0 = 0, last = -1;
-    if (nt > 0) {
-        c0 = ((rs + 1) * workers - 1) / total;  // the share that holds the item's first tile
-        if (share_start(c0 + 1, total, workers) >= re) return;  // finished by one worker
-        last = (re * workers - 1) / total;      // and its last one
-    }
+    const int2 range = pieces[blockIdx.x];
+    const int64_t c0 = range.x, last = range.y;
+    if (c0 == last) return;  // finished by one worker
     const ChunkGroup g = chunk_group<kTok, kKeys>(a, slot);
     const int rows = g.nq * kGrp, r0 = (blockIdx.y * kMergeWarps + warp) * kPer;
     if (r0 >= rows) return;
@@ -336,7 +385,6 @@ chunk_merge_many_kernel(const ChunkArgs a, const int64_t *__restrict__ prefix, i
         for (int j = 0; j < 8; ++j) acc[u][j] = 0.f;
     }
     for (int64_t c = c0; c <= last; ++c) {
-        if (c != c0 && share_start(c + 1, total, workers) == share_start(c, total, workers)) continue;  // an empty share
         const int64_t p = c == c0 ? 2 * c0 + 1 : 2 * c;
         float w[kPer], x[kPer][8];
 #pragma unroll
@@ -373,8 +421,8 @@ chunk_merge_many_kernel(const ChunkArgs a, const int64_t *__restrict__ prefix, i
     }
 }
 
-template <int kTok, int kKeys>
-cudaError_t launch_chunk_merge(const ChunkArgs &a, const int64_t *prefix, int64_t workers, cudaStream_t stream)
+template <int kTok, int kKeys, int kRestart>
+cudaError_t launch_chunk_merge(const ChunkArgs &a, const int2 *pieces, int64_t workers, cudaStream_t stream)
 {
     constexpr int kRows = kTok * kGrp;
     const int64_t items = 2 * chunk_slots<kTok>(a.total_q, a.batch);
@@ -385,12 +433,12 @@ cudaError_t launch_chunk_merge(const ChunkArgs &a, const int64_t *prefix, int64_
     const int64_t groups = a.total_q / kTok, some = a.batch < a.total_q ? a.batch : a.total_q;
     if (16 * (groups > some ? groups : some) <= workers) {
         const int64_t most = a.max_len_q < kTok ? (a.max_len_q > 0 ? a.max_len_q : 1) : kTok;
-        return launch_pdl(chunk_merge_kernel<kTok, kKeys>, dim3((unsigned)items, (unsigned)(most * kGrp)),
+        return launch_pdl(chunk_merge_kernel<kTok, kKeys, kRestart>, dim3((unsigned)items, (unsigned)(most * kGrp)),
                           dim3(kMergeThreads), 0, stream, a, workers);
     }
     constexpr int kPer = 4, kBlock = kMergeWarps * kPer;
     return launch_pdl(chunk_merge_many_kernel<kTok, kKeys, kPer>, dim3((unsigned)items, (kRows + kBlock - 1) / kBlock),
-                      dim3(kMergeThreads), 0, stream, a, prefix, workers);
+                      dim3(kMergeThreads), 0, stream, a, pieces, workers);
 }
 
 }  // namespace
