@@ -140,10 +140,10 @@ chunk_decode_kernel(const ChunkArgs a, int2 *__restrict__ pieces)
     const float c2 = a.scale * 1.4426950408889634f;
 
     while (at < te) {
-        ChunkGroup g = chunk_group<1, kDecKeys>(a, slot, &lengths);
+        ChunkGroup g = slot == share.slot ? share.g : chunk_group<1, kDecKeys>(ChunkDims(a, &lengths), slot);
         while (at >= first + 2 * (int64_t)g.nt) {  // empty slots between two tokens
             first += 2 * (int64_t)g.nt;
-            g = chunk_group<1, kDecKeys>(a, ++slot, &lengths);
+            g = chunk_group<1, kDecKeys>(ChunkDims(a, &lengths), ++slot);
         }
         const int hd = at >= first + g.nt ? 1 : 0;  // KV head
         const int64_t item = first + (int64_t)hd * g.nt;

@@ -284,7 +284,9 @@ __device__ __forceinline__ void transpose4(uint4 (&v)[4], int lane)
 }
 
 // The items of a share, in order: every role walks the same list.
-template <int kTok, int kKeys>
+// kCached: the first item's group as the share has it (e4m3: computed anew, the kernel's 128 registers fall
+// in a better order then, 3 % of a chunk).
+template <int kTok, int kKeys, bool kCached>
 struct TcWalk {
     const TcShared *sh;
     int64_t *state;  // shared memory, of this warp: next tile, its group's slot and that slot's first tile
@@ -313,10 +315,11 @@ struct TcWalk {
         int slot = (int)state[1];
         const int64_t te = sh->share.te;
         if (at >= te) return false;
-        ChunkGroup g = chunk_group<kTok, kKeys>(a, slot, &sh->lengths);
+        ChunkGroup g = kCached && slot == sh->share.slot ? sh->share.g
+                                                         : chunk_group_inline<kTok, kKeys>(ChunkDims(a, &sh->lengths), slot);
         while (at >= first + 2 * (int64_t)g.nt) {  // empty slots between two groups
             first += 2 * (int64_t)g.nt;
-            g = chunk_group<kTok, kKeys>(a, ++slot, &sh->lengths);
+            g = chunk_group_inline<kTok, kKeys>(ChunkDims(a, &sh->lengths), ++slot);
         }
         hd = at >= first + g.nt ? 1 : 0;
         const int64_t item = first + (int64_t)hd * g.nt;
@@ -478,7 +481,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = sh->tmem_base;
     volatile int *abort_flag = &sh->abort_flag;
-    TcWalk<C::kTok, kKeys> it(sh, sh->walk[warp]);
+    TcWalk<C::kTok, kKeys, !kFp8> it(sh, sh->walk[warp]);
     bool ok = true;
     if (warp == 0) {
         // ---------------- Q ----------------

@@ -55,23 +55,35 @@ struct ChunkLengths {
     }
 };
 
+// what a group follows from
+struct ChunkDims {
+    const int32_t *q, *k;
+    int batch, total_q, window, sinks;
+
+    __device__ __forceinline__ explicit ChunkDims(const ChunkArgs &a, const ChunkLengths *sh = nullptr)
+        : q(a.cu_q), k(a.cu_k), batch(a.batch), total_q((int)a.total_q), window((int)a.window), sinks((int)a.sinks)
+    {
+        if (sh != nullptr && batch <= kCuBatch) {
+            q = sh->q;
+            k = sh->k;
+        }
+    }
+};
+
 // (lengths and positions are int32, rows fewer than 2^28, sequences fewer than 2^28)
 template <int kTok, int kKeys>
-__device__ __forceinline__ ChunkGroup chunk_group(const ChunkArgs &a, int slot, const ChunkLengths *sh = nullptr)
+__device__ __forceinline__ ChunkGroup chunk_group_inline(const ChunkDims &a, int slot)
 {
-    const bool local = sh != nullptr && a.batch <= kCuBatch;
-    auto cu_q = [&](int i) -> int { return local ? sh->q[i] : __ldg(a.cu_q + i); };
-    auto cu_k = [&](int i) -> int { return local ? sh->k[i] : __ldg(a.cu_k + i); };
     ChunkGroup g;
     g.nt = g.ns = g.nq = 0;
     g.w_tile = g.row0 = g.t0 = 0;
     int lo = 0, hi = a.batch;  // the last s whose first slot is <= slot
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (cu_q(mid) / kTok + mid <= slot) lo = mid; else hi = mid;
+        if (a.q[mid] / kTok + mid <= slot) lo = mid; else hi = mid;
     }
     g.s = lo;
-    const int q0 = cu_q(lo), q1 = cu_q(lo + 1);
+    const int q0 = a.q[lo], q1 = a.q[lo + 1];
     const int first = (slot - (q0 / kTok + lo)) * kTok, Lq = q1 - q0;
     if (q0 < 0 || first < 0 || first >= Lq) return g;
     if (q1 > a.total_q) {  // lengths that the query tensor does not hold
@@ -80,12 +92,12 @@ __device__ __forceinline__ ChunkGroup chunk_group(const ChunkArgs &a, int slot, 
     }
     g.nq = Lq - first < kTok ? Lq - first : kTok;
     g.row0 = q0 + first;
-    g.t0 = cu_k(lo + 1) - cu_k(lo) - Lq + first;
+    g.t0 = a.k[lo + 1] - a.k[lo] - Lq + first;
     const int last = g.t0 + g.nq - 1;
     if (last < 0) return g;
     const int t_first = g.t0 > 0 ? g.t0 : 0;
-    const int w0 = a.window > 0 && t_first >= a.window ? t_first - (int)a.window + 1 : 0;
-    const int sinks = a.sinks < w0 ? (int)a.sinks : w0;
+    const int w0 = a.window > 0 && t_first >= a.window ? t_first - a.window + 1 : 0;
+    const int sinks = a.sinks < w0 ? a.sinks : w0;
     const int end = last / kKeys + 1;
     int ns = sinks / kKeys + (sinks % kKeys != 0 ? 1 : 0), w = w0 / kKeys;
     if (ns >= w) ns = w = 0;  // the sinks reach the window's first tile: one range from 0
@@ -93,6 +105,14 @@ __device__ __forceinline__ ChunkGroup chunk_group(const ChunkArgs &a, int slot, 
     g.w_tile = w;
     g.nt = ns + end - w;
     return g;
+}
+
+// One copy for the work list's several passes: the first fetches of their instructions took 1 us of a
+// small call.
+template <int kTok, int kKeys>
+static __device__ __noinline__ ChunkGroup chunk_group(ChunkDims a, int slot)
+{
+    return chunk_group_inline<kTok, kKeys>(a, slot);
 }
 
 // the group slots of a call (a host bound and the device's range)
@@ -106,6 +126,7 @@ struct ChunkShare {
     int64_t ts, te;       // this worker's tiles [ts, te) of the call's
     int64_t first;        // first tile of the group slot that holds ts
     int slot;             // that slot
+    ChunkGroup g;         // and its group
 };
 
 // x / y of numbers that mostly fit 32 bits
@@ -171,6 +192,80 @@ __device__ __forceinline__ void block_scan(int64_t x, int64_t y, int64_t *scan, 
     }
 }
 
+// an item's share of worker j of its n
+__device__ __forceinline__ void share_apart(ChunkShare *out, int slot, int64_t first, int64_t nt, int hd, int64_t j, int n)
+{
+    out->slot = slot;
+    out->first = first;
+    out->ts = first + hd * nt + divide(j * nt, n);
+    out->te = first + hd * nt + divide((j + 1) * nt, n);
+}
+
+// the shares that hold an item's first and last tile (even)
+__device__ __forceinline__ int2 even_pieces(int64_t at, int64_t nt, int64_t total, int64_t workers)
+{
+    if (nt == 0) return make_int2(0, -1);
+    return make_int2((int)divide((at + 1) * workers - 1, total), (int)divide((at + nt) * workers - 1, total));
+}
+
+// The same for up to 32 slots, by the first warp alone, without barriers between the steps (these and the
+// scans over the CTA took 3 us of a small call).
+template <int kTok, int kKeys, int kRestart>
+__device__ __forceinline__ void chunk_share_warp(const ChunkArgs &a, int64_t worker, int64_t workers, ChunkShare *out,
+                                                 int2 *pieces, const ChunkDims &dims, int slots)
+{
+    const int u = threadIdx.x;
+    const int64_t nt = u < slots ? chunk_group<kTok, kKeys>(dims, u).nt : 0;
+    int64_t incl = kHKV * nt;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+        if (u >= off) incl += x;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, incl, 31), before = incl - kHKV * nt;
+    const int items = kHKV * __popc(__ballot_sync(0xffffffffu, nt > 0));
+    if (u == 0) out->ts = out->te = out->first = out->slot = 0;
+    __syncwarp();
+    int2 p0 = make_int2(0, -1), p1 = p0;
+    bool holds = false;
+    if (total > 0) {  // uniform
+        const ChunkTotals t = chunk_totals<kRestart>(total, items, workers);
+        if (t.apart) {
+            const int n = item_workers((int)nt, t, workers);
+            int at = kHKV * n;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, at, off);
+                if (u >= off) at += x;
+            }
+            at -= kHKV * n;
+            p0 = make_int2(at, at + n - 1);
+            p1 = make_int2(at + n, at + 2 * n - 1);
+            holds = at <= worker && worker < at + kHKV * n;
+            if (holds) {
+                const int hd = worker - at >= n ? 1 : 0;
+                share_apart(out, u, before, nt, hd, worker - at - hd * n, n);
+            }
+        } else {
+            const int64_t ts = share_start(worker, total, workers), te = share_start(worker + 1, total, workers);
+            p0 = even_pieces(before, nt, total, workers);
+            p1 = even_pieces(before + nt, nt, total, workers);
+            holds = ts < te && before <= ts && ts < incl;
+            if (holds) {
+                out->slot = u;
+                out->first = before;
+                out->ts = ts;
+                out->te = te;
+            }
+        }
+    }
+    if (pieces != nullptr && u < slots) {
+        pieces[2 * u] = p0;
+        pieces[2 * u + 1] = p1;
+    }
+    if (holds) out->g = chunk_group<kTok, kKeys>(dims, u);
+}
+
 // This worker's share, by the whole CTA (whole warps); `scan`: two shared entries per warp.  `pieces`
 // (worker 0's CTA, or null): every item's first and last worker, for the merge; none: 0, -1.
 template <int kTok, int kKeys, int kThreads, int kRestart>
@@ -178,11 +273,25 @@ __device__ __forceinline__ void chunk_share(const ChunkArgs &a, int64_t worker, 
                                             int64_t *scan, int2 *pieces, const ChunkLengths *sh)
 {
     const int slots = (int)chunk_slots<kTok>(a.total_q, a.batch);
+    const ChunkDims dims(a, sh);
+    if (slots <= 32) {
+        if (threadIdx.x < 32) chunk_share_warp<kTok, kKeys, kRestart>(a, worker, workers, out, pieces, dims, slots);
+        __syncthreads();
+        return;
+    }
     const int per = (slots + kThreads - 1) / kThreads;  // consecutive slots of a thread
+    if (slots <= 32) {
+        if (threadIdx.x < 32) chunk_share_warp<kTok, kKeys, kRestart>(a, worker, workers, out, pieces, dims, slots);
+        __syncthreads();
+        return;
+    }
     const int u0 = (int)threadIdx.x * per < slots ? (int)threadIdx.x * per : slots, u1 = u0 + per < slots ? u0 + per : slots;
     int64_t mine = 0, items = 0;
+    int one = 0;  // the tiles of a thread's only slot
+    auto tiles_of = [&](int u) -> int { return per == 1 ? one : chunk_group<kTok, kKeys>(dims, u).nt; };
     for (int u = u0; u < u1; ++u) {
-        const int nt = chunk_group<kTok, kKeys>(a, u, sh).nt;
+        const int nt = chunk_group<kTok, kKeys>(dims, u).nt;
+        one = nt;
         mine += kHKV * (int64_t)nt;
         items += nt > 0 ? kHKV : 0;
     }
@@ -198,13 +307,13 @@ __device__ __forceinline__ void chunk_share(const ChunkArgs &a, int64_t worker, 
     const ChunkTotals t = chunk_totals<kRestart>(total, all, workers);
     if (t.apart) {
         int64_t wanted = 0, at_w, unused, all_w, unused_all;
-        for (int u = u0; u < u1; ++u) wanted += kHKV * item_workers(chunk_group<kTok, kKeys>(a, u, sh).nt, t, workers);
+        for (int u = u0; u < u1; ++u) wanted += kHKV * item_workers(tiles_of(u), t, workers);
         block_scan<kThreads>(wanted, 0, scan, at_w, unused, all_w, unused_all);
         const bool holds = at_w <= worker && worker < at_w + wanted;
         if (holds || pieces != nullptr) {
             int64_t at = before;
             for (int u = u0; u < u1; ++u) {
-                const int nt = chunk_group<kTok, kKeys>(a, u, sh).nt, n = item_workers(nt, t, workers);
+                const int nt = tiles_of(u), n = item_workers(nt, t, workers);
                 if (pieces != nullptr) {
                     pieces[2 * u] = make_int2((int)at_w, (int)at_w + n - 1);
                     pieces[2 * u + 1] = make_int2((int)at_w + n, (int)at_w + 2 * n - 1);
@@ -212,10 +321,8 @@ __device__ __forceinline__ void chunk_share(const ChunkArgs &a, int64_t worker, 
                 if (at_w <= worker && worker < at_w + kHKV * n) {
                     const int hd = worker - at_w >= n ? 1 : 0;
                     const int64_t j = worker - at_w - hd * n;
-                    out->slot = u;
-                    out->first = at;
-                    out->ts = at + hd * (int64_t)nt + divide(j * nt, n);
-                    out->te = at + hd * (int64_t)nt + divide((j + 1) * nt, n);
+                    share_apart(out, u, at, nt, hd, j, n);
+                    out->g = chunk_group<kTok, kKeys>(dims, u);
                 }
                 at += kHKV * (int64_t)nt;
                 at_w += kHKV * n;
@@ -227,17 +334,15 @@ __device__ __forceinline__ void chunk_share(const ChunkArgs &a, int64_t worker, 
         if (holds || pieces != nullptr) {
             int64_t at = before;
             for (int u = u0; u < u1; ++u) {
-                const int64_t nt = chunk_group<kTok, kKeys>(a, u, sh).nt;
+                const int64_t nt = tiles_of(u);
                 if (pieces != nullptr)
-                    for (int hd = 0; hd < kHKV; ++hd)  // the shares that hold the item's first and last tile
-                        pieces[2 * u + hd] = nt == 0 ? make_int2(0, -1)
-                                                     : make_int2((int)divide((at + hd * nt + 1) * workers - 1, total),
-                                                                 (int)divide((at + hd * nt + nt) * workers - 1, total));
+                    for (int hd = 0; hd < kHKV; ++hd) pieces[2 * u + hd] = even_pieces(at + hd * nt, nt, total, workers);
                 if (holds && at <= ts && ts < at + kHKV * nt) {
                     out->slot = u;
                     out->first = at;
                     out->ts = ts;
                     out->te = te;
+                    out->g = chunk_group<kTok, kKeys>(dims, u);
                 }
                 at += kHKV * nt;
             }
@@ -263,13 +368,14 @@ chunk_merge_kernel(const ChunkArgs a, int64_t workers)
     const int slot = blockIdx.x >> 1, slots = (int)chunk_slots<kTok>(a.total_q, a.batch);
     const int hd = blockIdx.x & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t tiles = 0, items = 0, p0 = 0, unused, total, all, before;
+    const ChunkDims dims(a);
     for (int u = threadIdx.x; u < slots; u += kMergeThreads) {
-        const int64_t nt = chunk_group<kTok, kKeys>(a, u).nt;
+        const int64_t nt = chunk_group<kTok, kKeys>(dims, u).nt;
         tiles += kHKV * nt;
         items += nt > 0 ? kHKV : 0;
         if (u < slot) p0 += kHKV * nt;
     }
-    const ChunkGroup g = chunk_group<kTok, kKeys>(a, slot);
+    const ChunkGroup g = chunk_group<kTok, kKeys>(ChunkDims(a), slot);
     block_scan<kMergeThreads>(tiles, items, scan, unused, unused, total, all);
     block_scan<kMergeThreads>(p0, 0, scan, unused, unused, before, unused);
     int64_t c0 = 0, last = -1;
@@ -278,7 +384,7 @@ chunk_merge_kernel(const ChunkArgs a, int64_t workers)
         if (t.apart) {
             int64_t wanted = 0, at_w;
             for (int u = threadIdx.x; u < slot; u += kMergeThreads)
-                wanted += kHKV * item_workers(chunk_group<kTok, kKeys>(a, u).nt, t, workers);
+                wanted += kHKV * item_workers(chunk_group<kTok, kKeys>(dims, u).nt, t, workers);
             block_scan<kMergeThreads>(wanted, 0, scan, unused, unused, at_w, unused);
             const int n = item_workers(g.nt, t, workers);
             c0 = at_w + hd * n;
@@ -372,7 +478,7 @@ chunk_merge_many_kernel(const ChunkArgs a, const int2 *__restrict__ pieces, int6
     const int2 range = pieces[blockIdx.x];
     const int64_t c0 = range.x, last = range.y;
     if (c0 == last) return;  // finished by one worker
-    const ChunkGroup g = chunk_group<kTok, kKeys>(a, slot);
+    const ChunkGroup g = chunk_group<kTok, kKeys>(ChunkDims(a), slot);
     const int rows = g.nq * kGrp, r0 = (blockIdx.y * kMergeWarps + warp) * kPer;
     if (r0 >= rows) return;
     const float *lse = a.ws + 2 * workers * kRows * kD;
