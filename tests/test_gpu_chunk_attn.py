@@ -288,6 +288,41 @@ def test_offsets_past_32_bits(qsa, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
+def test_calls_without_rows(qsa, fp8):
+    """No new tokens, no rows to read, no tokens to rotate: nothing is touched, nothing raises."""
+    pool = Pool([5, 9], 4, fp8).fill()
+    before = pool.k.view(torch.uint8).clone()
+    none = prefix([0, 0])
+    kv = torch.empty((0, HKV, D), dtype=torch.bfloat16, device="cuda")
+    qsa.cache_write_paged(kv, kv, pool.k, pool.v, pool.table, none, prefix(pool.lens), **pool.args())
+    k, v = qsa.cache_read_paged(pool.k, pool.v, pool.table, prefix(pool.lens), none, 0, **pool.args())
+    assert k.shape == v.shape == (0, HKV, D)
+    o, lse = qsa.chunk_attn_paged(torch.empty((0, HQ, D), dtype=torch.bfloat16, device="cuda"), pool.k, pool.v,
+                                  pool.table, none, prefix(pool.lens), 0, want_lse=True, **pool.args())
+    assert o.shape == (0, HQ, D) and lse.shape == (0, HQ)
+    qo, ko = qsa.rope_axes(o, k, torch.empty((3, 0), dtype=torch.int32, device="cuda"), (4, 2, 2))
+    assert qo.shape == o.shape and ko.shape == k.shape
+    assert torch.equal(pool.k.view(torch.uint8), before) and qsa.device_status(clear=True) == 0
+
+
+def test_host_tensors_are_refused(qsa):
+    pool = Pool([5], 4, False).fill()
+    cu = prefix([1])
+    q = queries(1)
+    with pytest.raises(ValueError):
+        qsa.chunk_attn_paged(q.cpu(), pool.k, pool.v, pool.table, cu, prefix([5]), 1)
+    with pytest.raises(ValueError):
+        qsa.chunk_attn_paged(q, pool.k, pool.v, pool.table.cpu(), cu, prefix([5]), 1)
+    with pytest.raises(qsa.QSAError):
+        qsa.chunk_attn_paged(q, pool.k, pool.v, pool.table, cu, prefix([5]), 1, o=q)
+    with pytest.raises(qsa.QSAError):
+        qsa.chunk_attn_paged(q, pool.k, pool.v, pool.table, cu, prefix([5]), 1,
+                             ws=torch.empty(100, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(qsa.QSAError):
+        qsa.rope_axes(q, None, torch.zeros((3, 1), dtype=torch.int32, device="cuda"), (100, 20, 20))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("most", [1, 5, 30])
 def test_large_batches(qsa, most, fp8):
     """More sequences than the kernels keep the lengths of at hand, some of them empty."""

@@ -168,3 +168,24 @@ def test_rope_axes_statuses(qsa):
         assert call(**bad) == qsa.QSA_ERR_INVALID_ARG, bad
     assert call(total=0) == qsa.QSA_OK
     assert call(q=0, k=0, qo=0, ko=0) == qsa.QSA_OK
+
+
+def test_constants_match_the_header(qsa):
+    import os
+    import re
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "qsa.h")).read()
+    defs = {n: int(v, 0) for n, v in re.findall(r"#define\s+(QSA_[A-Z0-9_]+)\s+([0-9x]+)u?\b", text)}
+    for name in ("QSA_CACHE_BF16", "QSA_CACHE_E4M3", "QSA_ROPE_INTERLEAVED", "QSA_ROPE_INVERSE"):
+        assert getattr(qsa, name) == defs[name], name
+    assert qsa.OP_CHUNK_PAGED == defs["QSA_OP_CHUNK_PAGED"]
+
+
+def test_workspace_holds_every_kernel(qsa):
+    """The workspace of any mix of lengths: pieces of two per worker, and two numbers per item of the
+    smallest groups."""
+    for batch, rows in ((1, 1), (64, 64), (3, 4096), (1000, 100000)):
+        need = qsa.workspace_size(qsa.OP_CHUNK_PAGED, batch, rows)
+        pairs = 2 * 80 * 252 * 257 * 4 + 2 * 8 * (rows // 10 + batch)
+        single = 2 * 160 * 12 * 257 * 4 + 2 * 8 * (rows + batch)
+        assert need >= max(pairs, single) and need % 4 == 0
