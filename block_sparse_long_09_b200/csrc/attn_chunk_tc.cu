@@ -19,8 +19,8 @@
 // 97 % of the copy rate; e4m3 394 us against a pair's 515).
 // Measured: 1024 new tokens over 16384, 1.38 PFLOP/s bf16, 1.17 e4m3; 2048 over 65536, bf16, 2.8 ms,
 // 1.17 PFLOP/s under the power cap (84 % of the sustained product rate).  A tile takes 2450 cycles in
-// bf16, bound by the chain S -> softmax -> O of 2300; 2900 in e4m3, where the softmax shares the
-// integer units with the conversion.
+// bf16, bound by the chain S -> softmax -> O of 2300; 2900 in e4m3, where the softmax shares its
+// schedulers with the conversion (seven integer operations and two products per four codes).
 //   warp 0       Q, once per item (TMA)
 //   warp 1       CTA 0: issues the products of both CTAs; CTA 1: passes on to CTA 0 that its Q and
 //                slots are full.  The fence between the slots' writers and the tensor cores stands
