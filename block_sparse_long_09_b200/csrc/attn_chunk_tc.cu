@@ -10,8 +10,8 @@
 //   S: M 256 N 128 K 256, Q and K from shared memory, two buffers of 128 TMEM columns
 //   O: M 256 N 256 K 128, P from TMEM (the first half of its S buffer, as bf16), V from shared
 //      memory; 256 TMEM columns, so the 512 columns of an SM are full
-// S(i + 1) is issued before O += P(i) V(i): the tensor cores run it while the softmax of
-// tile i is done, whose 128 exponentials per row (1024 cycles of an SM's exp2 units)
+// S(i + 1) is issued before O += P(i) V(i), and overwrites P(i - 1) behind the product that reads it (one
+// thread's products run in order): the tensor cores run it while the softmax of tile i is done, whose 128 exponentials per row (1024 cycles of an SM's exp2 units)
 // take half of the 2048 cycles of the tile's two products.
 // With at most 10 new tokens per sequence a CTA works alone (kCtas = 1): 128 rows, tiles of 64 keys.
 // The rows are mostly empty then and what counts is how fast keys are read: 148 CTAs that read
