@@ -308,9 +308,13 @@ struct TcWalk {
         __syncwarp();
     }
 
-    // by one lane or by all lanes of the warp together
+    // The next item, by all 32 lanes together (kWarp) or by one lane that walks for its warp.  All lanes have
+    // read the state before it is written, wherever they came from (a role may leave a divergent branch
+    // right before), and it is written before any of them reads it again.
+    template <bool kWarp>
     __device__ __forceinline__ bool next(const ChunkArgs &a)
     {
+        if (kWarp) __syncwarp();
         int64_t at = state[0], first = state[2];
         int slot = (int)state[1];
         const int64_t te = sh->share.te;
@@ -337,11 +341,13 @@ struct TcWalk {
         near = a.window > 0 ? t_first - (int)a.window + 1 : 0;
         sinks = (int)a.sinks;
         table = a.pool.table + (int64_t)s * a.pool.max_pages;
-        __syncwarp(__activemask());
-        state[0] = item + i1;  // (the same values from every lane)
-        state[1] = slot;
-        state[2] = first;
-        __syncwarp(__activemask());
+        if (kWarp) __syncwarp();
+        if (!kWarp || (threadIdx.x & 31) == 0) {
+            state[0] = item + i1;
+            state[1] = slot;
+            state[2] = first;
+        }
+        if (kWarp) __syncwarp();
         return true;
     }
 
@@ -486,7 +492,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
     if (warp == 0) {
         // ---------------- Q ----------------
         uint32_t n = 0;
-        while (ok && it.next(a)) {
+        while (ok && it.next<true>(a)) {
             ok = mbar_wait(&sh->q_empty, (n & 1) ^ 1, abort_flag);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             // Ten tokens, or of 21 CTA 0 the tokens 0 .. 9 and heads 0 .. 7 of token 10, CTA 1 its other heads and
@@ -547,7 +553,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                     advance();
                     return true;
                 };
-                while (ok && it.next(a)) {
+                while (ok && it.next<false>(a)) {
                     const int nt = it.i1 - it.i0;
                     ok = mbar_wait(&sh->q_full, n & 1, abort_flag) && (kCtas == 1 || wait_pair(&sh->q_peer, n & 1, abort_flag));
                     ok = ok && do_s(T);
@@ -575,7 +581,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                 }
             } else {
                 // ---------------- CTA 1: its Q and slots are full ----------------
-                while (ok && it.next(a)) {
+                while (ok && it.next<false>(a)) {
                     for (int e = 0; ok && e < 2 * (it.i1 - it.i0); ++e) {
                         ok = mbar_wait(&sh->kv_full[stage], ph, abort_flag);
                         fence_proxy_async_smem();
@@ -614,7 +620,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                     ph ^= 1u;
                 }
             };
-            while (ok && it.next(a)) {
+            while (ok && it.next<true>(a)) {
                 int32_t page[kCtas];
                 uint32_t off[kCtas] = {};
                 auto fetch = [&](int i) {
@@ -676,7 +682,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
             TcTable<kCtas> *tab = reinterpret_cast<TcTable<kCtas> *>(smem + C::kOffTable);
             const int key = (warp - 2) * 32 * kCtas + lane;
             uint32_t n = 0;  // tables written
-            while (ok && it.next(a)) {
+            while (ok && it.next<true>(a)) {
                 int32_t page[kCtas], row[kCtas];
                 uint32_t off[kCtas] = {}, kb[kCtas], vb[kCtas];
                 auto fetch = [&](int i) {
@@ -732,7 +738,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
             tc_fence_after();
             return ok;
         };
-        while (ok && it.next(a)) {
+        while (ok && it.next<true>(a)) {
             const int t = it.t0 + r / kGrp;  // this row's position (rows past the tokens: not written)
             float m = -INFINITY, l = 0.f;          // running maximum of c2 s, sum of exp2(c2 s - m)
             for (int i = it.i0; i < it.i1; ++i, ++T) {
@@ -955,7 +961,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                 ph ^= 1u;
             }
         };
-        while (ok && it.next(a)) {
+        while (ok && it.next<true>(a)) {
             const uint32_t nt = (uint32_t)(it.i1 - it.i0);
             if (!table_ready(n)) break;
             load_k(n % kTcTables);
