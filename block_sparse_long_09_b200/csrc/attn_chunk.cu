@@ -25,8 +25,10 @@
 //     Q is scaled by a power of two per row, its largest value into [2^14, 2^15): exact for
 //     values down to 2^-31 of the row's largest, off by 2^-39 of it below.
 //     The keys' scales multiply S.  The values' scales multiply P, p 2^e, which is held relative
-//     to the row's largest so far (a power of two, as the running maximum): 2^-12 relative,
-//     or below 2^-18 of the largest an absolute 2^-29 of it.
+//     to the row's largest so far (a power of two): 2^-12 relative, or below 2^-18 of the largest an
+//     absolute 2^-29 of it.  The running maximum moves by whole powers of two, and this reference
+//     with it, since what an early key left in O shrinks as the maximum grows: a late key far above the rest
+//     counts by its own size, however small its value's scale is beside theirs.
 //   * bf16 pools: P rounds to bf16, 2^-8 relative at most, as in every attention kernel here.
 //   * O is rescaled only when a row's maximum grows by more than 2^8.
 #include <cuda_fp16.h>
@@ -38,6 +40,7 @@ namespace qsa {
 namespace {
 
 constexpr int kDecWarps = 8, kDecThreads = kDecWarps * 32, kDecKeys = 16 * kDecWarps;
+constexpr int kUpRange = 110;   // e4m3: exponents of O's reference, -kUpRange .. kUpRange
 constexpr int kDecRestart = 2;  // tiles that another item on a worker costs (5 us, a tile 2.5)
 
 template <bool kFp8>
@@ -331,15 +334,28 @@ chunk_decode_kernel(const ChunkArgs a, int2 *__restrict__ pieces)
             for (int h = 0; h < 2; ++h) {
                 mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
                 mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+                if (kFp8) mx[h] = ceilf(mx[h]);
                 grow |= m[h] != -INFINITY && mx[h] > m[h] + 8.f;
             }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float to = fmaxf(m[h], mx[h]);
-                    const float f = m[h] == -INFINITY ? 1.f : dec_ex2(m[h] - to);
+                    float f;
+                    if (kFp8) {
+                        // the maximum is a whole number here: O's reference moves with it, and O stays as it is
+                        // held (but where the reference would leave its range)
+                        const int grown = m[h] == -INFINITY ? 0 : (int)fminf(to - m[h], 400.f);
+                        const int e = (int)(__float_as_uint(up[h]) >> 23) - 127;
+                        const int moved = up[h] == INFINITY ? 0 : min(grown, kUpRange - e);
+                        l[h] *= grown > 126 ? 0.f : pow2(-grown);
+                        if (moved > 0) up[h] = pow2(e + moved);
+                        f = grown - moved > 126 ? 0.f : pow2(moved - grown);
+                    } else {
+                        f = m[h] == -INFINITY ? 1.f : dec_ex2(m[h] - to);
+                        l[h] *= f;
+                    }
                     m[h] = to;
-                    l[h] *= f;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         o[j][2 * h] *= f;
@@ -371,7 +387,7 @@ chunk_decode_kernel(const ChunkArgs a, int2 *__restrict__ pieces)
                         px[h] = fmaxf(px[h], __shfl_xor_sync(0xffffffffu, px[h], 1));
                         px[h] = fmaxf(px[h], __shfl_xor_sync(0xffffffffu, px[h], 2));
                         if (px[h] * up[h] > 32768.f) {
-                            const float to = pow2(min(max(131 - (int)(__float_as_uint(px[h]) >> 23), -110), 110));
+                            const float to = pow2(min(max(131 - (int)(__float_as_uint(px[h]) >> 23), -kUpRange), kUpRange));
                             const float f = up[h] == INFINITY ? 0.f : to / up[h];  // (powers of two)
                             up[h] = to;
 #pragma unroll
