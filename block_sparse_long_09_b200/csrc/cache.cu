@@ -9,7 +9,8 @@
 //          back and written again gives the same codes.  A scale max|x| / 448 would use the
 //          codes' last factor of two at most, for a division per value and a second rounding.
 //          A row that holds an infinity or a NaN is stored as the byte 255 with zero codes
-//          and reads back as NaN: the codes themselves are always finite.
+//          and reads back as NaN.  The codes that are written are finite; a pool filled otherwise may
+//          hold the type's NaN codes, which read back as NaN.
 //
 // Bound by HBM in both directions (2 KB of bf16 and 1028 B of e4m3 per token).  Writing: a warp
 // per (token, K or V): both heads' 512 values are 16 per lane, 32 bytes of bf16 memory and one
@@ -98,10 +99,10 @@ cache_write_kernel(const __nv_bfloat16 *__restrict__ k, const __nv_bfloat16 *__r
     if ((lane & 15) == 0) (is_v ? c.v_scales : c.k_scales)[row * 2 + (lane >> 4)] = (uint8_t)byte;
 }
 
-// an e4m3 code's value: its 7 low bits are the top of an fp32 whose exponent is 120 too low
-__device__ __forceinline__ float e4m3_to_float(uint32_t code)
+// two e4m3 codes' values (the type's NaN codes, 0x7F and 0xFF, among them)
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t two)
 {
-    return __uint_as_float(((code & 0x80u) << 24) | ((code & 0x7Fu) << 20)) * 0x1p120f;
+    return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3)));
 }
 
 template <bool kFp8>
@@ -159,9 +160,8 @@ cache_read_kernel(const CachePool c, const int32_t *__restrict__ cu_k, const int
         uint32_t out[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t two = w[j >> 1] >> (16 * (j & 1));
-            const __nv_bfloat162 p = __floats2bfloat162_rn(e4m3_to_float(two & 0xFFu) * scale,
-                                                           e4m3_to_float((two >> 8) & 0xFFu) * scale);
+            const float2 x = e4m3x2_to_float2((w[j >> 1] >> (16 * (j & 1))) & 0xFFFFu);
+            const __nv_bfloat162 p = __floats2bfloat162_rn(x.x * scale, x.y * scale);
             out[j] = *reinterpret_cast<const uint32_t *>(&p);
         }
         // a lane's 16 values are two pieces of 16 bytes; two lanes exchange one, so that a store covers
