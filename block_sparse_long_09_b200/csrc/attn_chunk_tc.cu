@@ -20,7 +20,7 @@
 // Measured: 1024 new tokens over 16384, 1.38 PFLOP/s bf16, 1.17 e4m3; 2048 over 65536, bf16, 2.8 ms,
 // 1.17 PFLOP/s under the power cap (84 % of the sustained product rate).  A tile takes 2450 cycles in
 // bf16, bound by the chain S -> softmax -> O of 2300; 2900 in e4m3, where the softmax shares its
-// schedulers with the conversion (seven integer operations and two products per four codes).
+// schedulers with the conversion (ten operations per four codes).
 //   warp 0       Q, once per item (TMA)
 //   warp 1       CTA 0: issues the products of both CTAs; CTA 1: passes on to CTA 0 that its Q and
 //                slots are full.  The fence between the slots' writers and the tensor cores stands
@@ -31,9 +31,11 @@
 //                e4m3 pools: the pool rows and scales of the tiles' keys, into a ring of tables
 //   warps 4..7   softmax, a thread per row; running maxima move (and O is rescaled) only when a
 //                row's maximum grows by more than 2^8
-//   warps 8..15  (e4m3 pools) codes to bf16 in registers, exactly: the 7 low bits moved to the
-//                top of a bf16, times 2^120 times the row's scale; then to one of four slots
+//   warps 8..15  (e4m3 pools) codes to bf16 in registers, exactly, times the row's scale; then to one of
+//                four slots
 // Work is shared out and cut items are merged as chunk_common.cuh describes.  Every wait is bounded.
+#include <cuda_fp16.h>
+
 #include <mutex>
 
 #include "chunk_common.cuh"
@@ -258,6 +260,12 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t r;
@@ -383,44 +391,33 @@ struct TcWalk {
     }
 };
 
-// 16 e4m3 codes -> 16 bf16 values times s1 (and s2)
-__device__ __forceinline__ uint32_t bmul2(uint32_t x, uint32_t s)
-{
-    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), *reinterpret_cast<const __nv_bfloat162 *>(&s));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-
-// A code's sign and its 7 low bits, put at the top of a bf16, are its value times 2^-120.  A row's
-// scale 2^(byte - 127) and 2^120 are one bf16 factor up to byte 134, two beyond (byte 255: NaN).
-struct RowScale {
-    uint32_t s1, s2;
-    bool two;
-};
-__device__ __forceinline__ RowScale row_scale(uint32_t byte)
-{
-    RowScale r;
-    const uint32_t b1 = byte == 255u ? 0x7FC0u : ((byte > 134u ? 254u : byte + 120u) << 7);
-    const uint32_t b2 = byte > 134u ? (byte - 7u) << 7 : 0x3F80u;
-    r.s1 = b1 * 0x10001u;
-    r.s2 = b2 * 0x10001u;
-    r.two = byte > 134u;
-    return r;
-}
-
-__device__ __forceinline__ void codes_to_slot(const uint4 &codes, const RowScale &sc, uint32_t row_addr, uint32_t unit,
-                                              uint32_t sw)
+// 16 e4m3 codes -> 16 bf16 values times their row's scale, in a slot.  By the conversion instructions, which
+// give NaN for the type's NaN codes (shifts and masks take them for 480; with a test for them beside the shifts
+// the calls below took 12 % longer).  fp16, fp32 and bf16 hold a code exactly, and times a power of two too.  The
+// scale goes to the fp32 values in a pair (four prompts' chunks 289 against 297 us as bf16 products), to the bf16
+// ones in a single CTA (four tokens over 32 caches 418 against 465 us as fp32 products).
+template <int kCtas>
+__device__ __forceinline__ void codes_to_slot(const uint4 &codes, float scale, uint32_t row_addr, uint32_t unit, uint32_t sw)
 {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    const uint64_t s2 = pack2(scale, scale);
     uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t hi = (w[i] & 0x80808080u) | ((w[i] >> 4) & 0x07070707u), lo = (w[i] << 4) & 0xF0F0F0F0u;
-        o[2 * i] = bmul2(__byte_perm(lo, hi, 0x5140), sc.s1);
-        o[2 * i + 1] = bmul2(__byte_perm(lo, hi, 0x7362), sc.s1);
-    }
-    if (sc.two) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = bmul2(o[i], sc.s2);
+    for (int i = 0; i < 8; ++i) {
+        uint32_t h;
+        asm("{\n\t.reg .b16 lo, hi;\n\t"
+            "mov.b32 {lo, hi}, %1;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+            : "=r"(h) : "r"(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        if (kCtas == 2) {
+            const float2 x = unpack2(mul2(pack2(f.x, f.y), s2));
+            const __nv_bfloat162 r = __floats2bfloat162_rn(x.x, x.y);
+            o[i] = *reinterpret_cast<const uint32_t *>(&r);
+        } else {
+            const __nv_bfloat162 r = __hmul2(__floats2bfloat162_rn(f.x, f.y), __float2bfloat162_rn(scale));
+            o[i] = *reinterpret_cast<const uint32_t *>(&r);
+        }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -968,10 +965,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
             for (uint32_t i = 0; i <= nt; ++i) {
                 if (i < nt) {  // K(i)
                     if (!slot_ready()) break;
-                    const RowScale sc = row_scale(kb);
+                    const float sc = scale_of_byte(kb);
                     const uint32_t dst = ring_u + stage * kTcSlot + (cw * 8 + k8) * 128;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) codes_to_slot(kreg[c], sc, dst + c * kTcKChunk, 2 * piece, k8);
+                    for (int c = 0; c < 4; ++c) codes_to_slot<kCtas>(kreg[c], sc, dst + c * kTcKChunk, 2 * piece, k8);
                     slot_done();
                 }
                 if (i + 1 < nt) {
@@ -982,10 +979,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                     if (!slot_ready()) break;
 #pragma unroll
                     for (int q = 0; q < kCtas; ++q) {
-                        const RowScale sc = row_scale(vb[q]);
+                        const float sc = scale_of_byte(vb[q]);
                         const uint32_t dst = ring_u + stage * kTcSlot + ((cw * kCtas + q) * 8 + k8) * 128;
 #pragma unroll
-                        for (int c = 0; c < C::kVChunks; ++c) codes_to_slot(vreg[q * C::kVChunks + c], sc, dst + c * C::kVChunk, 2 * piece, k8);
+                        for (int c = 0; c < C::kVChunks; ++c) codes_to_slot<kCtas>(vreg[q * C::kVChunks + c], sc, dst + c * C::kVChunk, 2 * piece, k8);
                     }
                     slot_done();
                 }

@@ -484,6 +484,7 @@ qsa_status qsa_dense_attn_prefill(const qsa_config *cfg, const qsa_bf16 *q, cons
  *       QSA_CACHE_BF16  the values
  *       QSA_CACHE_E4M3  8-bit codes (4 exponent, 3 mantissa bits, largest 448) with one scale
  *                       byte per (token, KV head):  value = code * 2^(byte - 127)
+ *                       (NaN for the byte 255 and for the type's NaN codes 0x7F and 0xFF)
  *   k_scales, v_scales [num_pages, page_size, n_heads_kv] uint8 (E4M3; ignored for BF16)
  *   block_table       [batch, max_pages] int32: page j of sequence s holds its tokens
  *                     [j page_size, (j + 1) page_size)
