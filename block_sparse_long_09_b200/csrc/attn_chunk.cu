@@ -374,8 +374,9 @@ chunk_decode_kernel(const ChunkArgs a, int2 *__restrict__ pieces)
                     for (int x = 0; x < 2; ++x) {
                         const float e = dec_ex2(s[y][2 * h + x] - base[h]);
                         l[h] += e;
-                        // a hidden key's scale may be a NaN (a row with a non-finite value): P stays 0
-                        p[h][y][x] = kFp8 ? (e == 0.f ? 0.f : e * vs[y][x]) : e;
+                        // (a key that the row does not see has the scale 1; a NaN scale of one that it
+                        // sees makes a NaN of the row however small its probability)
+                        p[h][y][x] = kFp8 ? e * vs[y][x] : e;
                         px[h] = fmaxf(px[h], p[h][y][x]);
                     }
             }

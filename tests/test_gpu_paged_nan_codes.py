@@ -78,7 +78,7 @@ def test_key_codes(qsa, n, code):
         assert not torch.isnan(o[:, :12]).any() and not torch.isnan(lse[:, :12]).any()
 
 
-@pytest.mark.parametrize("what", ["code"])
+@pytest.mark.parametrize("what", ["byte", "code"])
 @pytest.mark.parametrize("n", [1, 4, 64])
 def test_values_of_keys_whose_probability_underflows(qsa, n, what):
     """A key 200 powers of two below the rest is seen all the same: its NaN reaches the row."""
