@@ -281,7 +281,7 @@ size_t qsa_workspace_size(const qsa_config *cfg, int32_t op, int32_t batch, int6
 qsa_status qsa_debug_inject(int32_t site)
 {
 #ifdef QSA_DEBUG_CHECKS
-    if (site < 0 || site > 1) return QSA_ERR_INVALID_ARG;
+    if (site < 0 || site > 2) return QSA_ERR_INVALID_ARG;
     int v = site;
     return cudaMemcpyToSymbol(g_debug_fault_site, &v, sizeof(int)) == cudaSuccess ? QSA_OK : QSA_ERR_CUDA;
 #else

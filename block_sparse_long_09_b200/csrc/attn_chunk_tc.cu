@@ -55,7 +55,7 @@ struct TcShared {
     uint64_t kv_full[kTcMaxStages], kv_peer[kTcMaxStages], kv_empty[kTcMaxStages];
     uint64_t q_full, q_peer, q_empty;
     uint64_t s_full[2], p_full[2];
-    uint64_t pv_done, o_full, o_empty;
+    uint64_t pv_done, o_full, o_empty, drained;
     uint64_t tab_full[kTcTables], tab_empty[kTcTables];
     uint32_t tmem_base;
     int abort_flag;
@@ -455,6 +455,7 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
             mbar_init(&sh->p_full[i], 4 * kCtas);
         }
         mbar_init(&sh->pv_done, 1);
+        mbar_init(&sh->drained, 1);
         mbar_init(&sh->o_full, 1);
         mbar_init(&sh->o_empty, 4 * kCtas);
         for (int i = 0; i < kTcTables; ++i) {
@@ -516,6 +517,8 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
             __syncwarp();
             ++n;
         }
+        // where a role has given up, the last copies may be on their way still: they land before the CTA exits
+        if (lane == 0 && n > 0) mbar_wait(&sh->q_full, (n - 1) & 1, nullptr);
     } else if (warp == 1) {
         if (elect_one()) {
             uint32_t stage = 0, ph = 0, n = 0;
@@ -576,6 +579,10 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                     }
                     ++n;
                 }
+                // and likewise the products that have been issued: no tensor memory is freed under them (CTA 1
+                // waits for this CTA at the end)
+                commit_all<kCtas>(&sh->drained);
+                mbar_wait(&sh->drained, 0, nullptr);
             } else {
                 // ---------------- CTA 1: its Q and slots are full ----------------
                 while (ok && it.next<false>(a)) {
@@ -609,7 +616,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
                 const bool good = mbar_wait(&sh->kv_empty[stage], ph, abort_flag);
                 return __all_sync(0xffffffffu, good);
             };
+#ifdef QSA_DEBUG_CHECKS
+            // injected fault: the second slot of CTA 1, or of the only CTA, is never full
+            bool withhold = g_debug_fault_site == 2 && rank == kCtas - 1;
+#endif
             auto slot_issued = [&]() {
+#ifdef QSA_DEBUG_CHECKS
+                if (withhold && stage == 1) withhold = false;
+                else
+#endif
                 asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];"
                              ::"r"(smem_u32(&sh->kv_full[stage])) : "memory");
                 if (++stage == C::kStages) {
@@ -950,8 +965,15 @@ chunk_tc_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant
             ok = mbar_wait(&sh->kv_empty[stage], ph, abort_flag);
             return ok = __all_sync(0xffffffffu, ok);
         };
+#ifdef QSA_DEBUG_CHECKS
+        bool withhold = g_debug_fault_site == 2 && rank == kCtas - 1;  // as above
+#endif
         auto slot_done = [&]() {
             __syncwarp();
+#ifdef QSA_DEBUG_CHECKS
+            if (withhold && stage == 1) withhold = false;
+            else
+#endif
             if (lane == 0) mbar_arrive(&sh->kv_full[stage]);
             if (++stage == C::kStages) {
                 stage = 0;

@@ -602,6 +602,9 @@ int32_t qsa_version(void);
  *           copies for the second kc tile of each CTA, so the consumer's bounded
  *           wait runs out: the call's kernels return, the status word reads
  *           QSA_ERR_TIMEOUT and the next call without the fault runs normally.
+ *   site 2  qsa_chunk_attn_paged (calls that reach its tensor-core kernel): the second half
+ *           tile of K or V of each item's last CTA never counts as arrived, so the waits of both
+ *           CTAs of a pair, or of the only one, run out, with the same outcome.
  * Host only (one device-symbol copy); not thread-safe with calls in flight. */
 qsa_status qsa_debug_inject(int32_t site);
 
