@@ -5,9 +5,12 @@
 //   e4m3   x ~ code * 2^e with one exponent per row, the smallest e >= -127 with
 //          max|x| <= 448 * 2^e, stored as the byte e + 127; code = x * 2^-e rounded to
 //          nearest even.  A power of two makes both directions exact but for that one
-//          rounding: x * 2^-e is exact in fp32, code * 2^e is exact in bf16, so a row read
-//          back and written again gives the same codes.  A scale max|x| / 448 would use the
-//          codes' last factor of two at most, for a division per value and a second rounding.
+//          rounding: x * 2^-e is exact in fp32, code * 2^e is exact in bf16.  A row that is
+//          written, read back and written again has the same values; its codes and byte are
+//          the same too, or the byte is one less and the codes stand for twice as much (a maximum just
+//          above 448 * 2^e that was rounded down to it: 450 is held as 224 * 2, and 448 then as
+//          448 * 1).  A scale max|x| / 448 would use the codes' last factor of two at most,
+//          for a division per value and a second rounding.
 //          A row that holds an infinity or a NaN is stored as the byte 255 with zero codes
 //          and reads back as NaN.  The codes that are written are finite; a pool filled otherwise may
 //          hold the type's NaN codes, which read back as NaN.
