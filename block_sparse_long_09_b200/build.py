@@ -4,8 +4,9 @@ libqsa_debug.so is the same sources built with QSA_DEBUG_CHECKS: mbarrier waits
 limited to 20 ms and the fault-injection site of qsa_debug_inject compiled in.
 Only the failure-path tests load it (QSA_DEBUG_BUILD=1 in their child process).
 
-_binding.so is csrc/binding.cpp (tensor checks of the paged-cache calls) against torch's
-headers, by the C++ compiler; it calls whichever of the two libraries is loaded.
+_binding_<torch version>_<Python ABI>.so is csrc/binding.cpp (tensor checks of the paged-cache calls)
+against torch's headers, by the C++ compiler; it calls whichever of the two libraries is loaded.  It holds
+for the torch and the Python that it was built with: under others it counts as not built.
 
 Usage: python -m block_sparse_long_09_b200.build [--force] [--verbose] [--debug | --all]
 """
@@ -22,7 +23,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libqsa.so")
 LIB_DEBUG = os.path.join(HERE, "libqsa_debug.so")
-BINDING = os.path.join(HERE, "_binding.so")
 BINDING_SRC = os.path.join(CSRC, "binding.cpp")
 DEBUG_FLAGS = ["-DQSA_DEBUG_CHECKS=1", "-DQSA_WAIT_LIMIT_NS=20000000ull"]
 
@@ -32,6 +32,18 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-shared",
     "--expt-relaxed-constexpr",
 ]
+
+
+def binding_path() -> str:
+    """The compiled binding's file for the running torch and Python."""
+    import sysconfig
+
+    import torch
+    return os.path.join(HERE, "_binding_torch%s_%s.so" % (torch.__version__, sysconfig.get_config_var("SOABI")))
+
+
+def is_binding(lib: str) -> bool:
+    return os.path.basename(lib).startswith("_binding_")
 
 
 def sources():
@@ -47,7 +59,7 @@ def needs_build(lib: str = LIB) -> bool:
         return True
     t = os.path.getmtime(lib)
     return any(os.path.getmtime(p) > t for p in
-               ([BINDING_SRC, os.path.join(INCLUDE, "qsa.h")] if lib == BINDING else deps()))
+               ([BINDING_SRC, os.path.join(INCLUDE, "qsa.h")] if is_binding(lib) else deps()))
 
 
 def _binding_command(tmp: str):
@@ -65,7 +77,7 @@ def _binding_command(tmp: str):
 
 
 def _command(lib: str, tmp: str, verbose: bool):
-    if lib == BINDING:
+    if is_binding(lib):
         return _binding_command(tmp)
     nvcc = os.environ.get("NVCC", "nvcc")
     cmd = [nvcc] + NVCC_FLAGS + (DEBUG_FLAGS if lib == LIB_DEBUG else []) + \
@@ -77,7 +89,7 @@ def _command(lib: str, tmp: str, verbose: bool):
 
 
 def build_libs(libs, force: bool = False, verbose: bool = False):
-    """Build the given libraries (LIB, LIB_DEBUG, BINDING) that are missing or stale, in parallel."""
+    """Build the given libraries (LIB, LIB_DEBUG, the binding) that are missing or stale, in parallel."""
     todo = [lib for lib in libs if force or needs_build(lib)]
     procs = []
     for lib in todo:
@@ -92,11 +104,11 @@ def build_libs(libs, force: bool = False, verbose: bool = False):
 
 
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
-    return build_libs([LIB_DEBUG if debug else LIB, BINDING], force, verbose)[0]
+    return build_libs([LIB_DEBUG if debug else LIB, binding_path()], force, verbose)[0]
 
 
 def build_all(force: bool = False, verbose: bool = False):
-    return build_libs([LIB, LIB_DEBUG, BINDING], force, verbose)
+    return build_libs([LIB, LIB_DEBUG, binding_path()], force, verbose)
 
 
 if __name__ == "__main__":

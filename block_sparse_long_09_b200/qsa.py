@@ -135,10 +135,17 @@ _DEFAULT_ADDR = ctypes.addressof(_DEFAULT_CFG)
 
 def _bind():
     """The compiled argument checks of the paged-cache calls, which call the library loaded here."""
+    from importlib.machinery import ExtensionFileLoader
+    from importlib.util import module_from_spec, spec_from_file_location
+
+    from .build import binding_path
+    path, name = binding_path(), __package__ + "._binding"
     try:
-        from . import _binding as b
+        spec = spec_from_file_location(name, path, loader=ExtensionFileLoader(name, path))
+        b = module_from_spec(spec)
+        spec.loader.exec_module(b)
     except ImportError as e:
-        raise ImportError("_binding.so is missing or does not load; build it with "
+        raise ImportError(f"{path} is missing or does not load; build it with "
                           "'python -m block_sparse_long_09_b200.build'") from e
     b.bind(*(ctypes.cast(getattr(_lib, f), ctypes.c_void_p).value for f in
              ("qsa_cache_write_paged", "qsa_cache_read_paged", "qsa_chunk_attn_paged", "qsa_rope_axes",
@@ -146,7 +153,17 @@ def _bind():
     return b
 
 
-_binding = _bind()
+class _Unbound:
+    """Stands for the compiled binding until the first paged-cache call: it depends on torch's and Python's versions,
+    which the other calls do not, so they work without it."""
+
+    def __getattr__(self, name):
+        global _binding
+        _binding = _bind()
+        return getattr(_binding, name)
+
+
+_binding = _Unbound()
 
 
 def _check(status: int, where: str):
