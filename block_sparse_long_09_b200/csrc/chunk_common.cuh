@@ -351,6 +351,7 @@ __device__ __forceinline__ void chunk_share(const ChunkArgs &a, int64_t worker, 
     __syncthreads();
 }
 
+constexpr int kMergeScan = 32;  // group slots that the first merge's CTAs scan, at most
 constexpr int kMergeWarps = 8, kMergeThreads = kMergeWarps * 32;
 static_assert(kMergeThreads == kD, "a thread per dim");
 
@@ -369,13 +370,17 @@ chunk_merge_kernel(const ChunkArgs a, int64_t workers)
     const int hd = blockIdx.x & 1, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t tiles = 0, items = 0, p0 = 0, unused, total, all, before;
     const ChunkDims dims(a);
+    const ChunkGroup g = chunk_group<kTok, kKeys>(dims, slot);
+    if (blockIdx.y >= g.nq * kGrp) {  // uniform for the CTA: no such row, before the scan over all slots
+        pdl_enter();
+        return;
+    }
     for (int u = threadIdx.x; u < slots; u += kMergeThreads) {
         const int64_t nt = chunk_group<kTok, kKeys>(dims, u).nt;
         tiles += kHKV * nt;
         items += nt > 0 ? kHKV : 0;
         if (u < slot) p0 += kHKV * nt;
     }
-    const ChunkGroup g = chunk_group<kTok, kKeys>(ChunkDims(a), slot);
     block_scan<kMergeThreads>(tiles, items, scan, unused, unused, total, all);
     block_scan<kMergeThreads>(p0, 0, scan, unused, unused, before, unused);
     int64_t c0 = 0, last = -1;
@@ -397,7 +402,7 @@ chunk_merge_kernel(const ChunkArgs a, int64_t workers)
     }
     const int rows = g.nq * kGrp;
     pdl_enter();
-    if (blockIdx.y >= rows || (g.nt > 0 && last == c0)) return;  // uniform for the CTA; finished by one worker
+    if (g.nt > 0 && last == c0) return;  // uniform for the CTA: finished by one worker
     const float *lse = a.ws + 2 * workers * kRows * kD;
     for (int r = blockIdx.y; r < rows; r += gridDim.y) {
         float mx = -INFINITY, sum = 0.f, acc[8];
@@ -535,9 +540,11 @@ cudaError_t launch_chunk_merge(const ChunkArgs &a, const int2 *pieces, int64_t w
     if (items > 0x7FFFFFFF) return cudaErrorInvalidValue;
     // Items that are cut into eight pieces or more: a CTA per row, its eight warps over the row's pieces
     // (one sequence of 8191 cached tokens: 4 us less); otherwise a warp per four rows, whose lookups
-    // cost less (batch 64 of decoded tokens: 20 us less).
+    // cost less (batch 64 of decoded tokens: 20 us less).  A few tokens in a batch that is mostly empty go the
+    // second way too: the CTAs of the first each scan all group slots (four tokens, e4m3, 1000 cached
+    // ones each, 22 and 22 us among 16 sequences, 27 and 25 us among 64, 103 and 47 us among 1024).
     const int64_t groups = a.total_q / kTok, some = a.batch < a.total_q ? a.batch : a.total_q;
-    if (16 * (groups > some ? groups : some) <= workers) {
+    if (16 * (groups > some ? groups : some) <= workers && items <= 2 * kMergeScan) {
         const int64_t most = a.max_len_q < kTok ? (a.max_len_q > 0 ? a.max_len_q : 1) : kTok;
         return launch_pdl(chunk_merge_kernel<kTok, kKeys, kRestart>, dim3((unsigned)items, (unsigned)(most * kGrp)),
                           dim3(kMergeThreads), 0, stream, a, workers);
