@@ -280,11 +280,6 @@ __device__ __forceinline__ void chunk_share(const ChunkArgs &a, int64_t worker, 
         return;
     }
     const int per = (slots + kThreads - 1) / kThreads;  // consecutive slots of a thread
-    if (slots <= 32) {
-        if (threadIdx.x < 32) chunk_share_warp<kTok, kKeys, kRestart>(a, worker, workers, out, pieces, dims, slots);
-        __syncthreads();
-        return;
-    }
     const int u0 = (int)threadIdx.x * per < slots ? (int)threadIdx.x * per : slots, u1 = u0 + per < slots ? u0 + per : slots;
     int64_t mine = 0, items = 0;
     int one = 0;  // the tiles of a thread's only slot
