@@ -196,6 +196,19 @@ bool in_pool(const qsa_config *c, const void *p, int64_t bytes, int32_t format, 
     return format == QSA_CACHE_E4M3 && (overlap(p, bytes, k_scales, rows) || overlap(p, bytes, v_scales, rows));
 }
 
+// do two of the pool's arrays share memory (a pool that is only read may have K and V in one)
+bool pool_overlaps_itself(const qsa_config *c, int32_t format, const void *k_pages, const void *v_pages,
+                          const uint8_t *k_scales, const uint8_t *v_scales, int64_t num_pages, int32_t page_size)
+{
+    const int64_t rows = num_pages * page_size * c->n_heads_kv;
+    const int64_t codes = rows * c->head_dim * (format == QSA_CACHE_E4M3 ? 1 : 2);
+    if (overlap(k_pages, codes, v_pages, codes)) return true;
+    if (format != QSA_CACHE_E4M3) return false;
+    for (const uint8_t *s : {k_scales, v_scales})
+        if (overlap(s, rows, k_pages, codes) || overlap(s, rows, v_pages, codes)) return true;
+    return overlap(k_scales, rows, v_scales, rows);
+}
+
 qsa::CachePool pool_of(int32_t format, const void *k_pages, const void *v_pages, const uint8_t *k_scales,
                        const uint8_t *v_scales, int64_t num_pages, int32_t page_size, const int32_t *block_table,
                        int32_t max_pages)
@@ -690,6 +703,8 @@ qsa_status qsa_cache_write_paged(const qsa_config *cfg, const qsa_bf16 *k, const
     if (st != QSA_OK) return st;
     if (total_q == 0) return QSA_OK;
     if (k == nullptr || v == nullptr || !al16(k) || !al16(v)) return QSA_ERR_INVALID_ARG;
+    if (pool_overlaps_itself(cfg, format, k_pages, v_pages, k_scales, v_scales, num_pages, page_size))
+        return QSA_ERR_INVALID_ARG;
     for (const qsa_bf16 *p : {k, v})
         if (in_pool(cfg, p, total_q * cfg->n_heads_kv * cfg->head_dim * 2, format, k_pages, v_pages, k_scales,
                     v_scales, num_pages, page_size))
@@ -746,11 +761,19 @@ qsa_status qsa_chunk_attn_paged(const qsa_config *cfg, const qsa_bf16 *q, int32_
     if (ws == nullptr || ws_bytes < chunk_workspace_bytes(batch, total_q)) return QSA_ERR_WORKSPACE_TOO_SMALL;
     if (!al16(ws)) return QSA_ERR_INVALID_ARG;
     const int64_t q_bytes = total_q * cfg->n_heads_q * cfg->head_dim * 2;
-    if (overlap(q, q_bytes, o, q_bytes)) return QSA_ERR_INVALID_ARG;
-    for (const void *p : {static_cast<const void *>(o), static_cast<const void *>(lse)})
-        if (in_pool(cfg, p, p == o ? q_bytes : total_q * cfg->n_heads_q * 4, format, k_pages, v_pages, k_scales,
-                    v_scales, num_pages, page_size))
+    // o, lse and the workspace share no memory with each other, with q or with the pool
+    struct Range {
+        const void *p;
+        int64_t bytes;
+    };
+    const Range out[] = {{o, q_bytes}, {lse, total_q * cfg->n_heads_q * 4},
+                         {ws, (int64_t)chunk_workspace_bytes(batch, total_q)}, {q, q_bytes}};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return QSA_ERR_INVALID_ARG;
+        if (in_pool(cfg, out[i].p, out[i].bytes, format, k_pages, v_pages, k_scales, v_scales, num_pages, page_size))
             return QSA_ERR_INVALID_ARG;
+    }
     ChunkArgs a{bf(q), pool_of(format, k_pages, v_pages, k_scales, v_scales, num_pages, page_size, block_table, max_pages),
                 cu_seqlens_q, cu_seqlens_k, batch, total_q, max_len_q, window, sinks, cfg->softmax_scale, bf(o), lse,
                 static_cast<float *>(ws)};
@@ -780,7 +803,8 @@ qsa_status qsa_rope_axes(const qsa_config *cfg, const qsa_bf16 *q, const qsa_bf1
     const int64_t q_bytes = total * cfg->n_heads_q * cfg->head_dim * 2, k_bytes = total * cfg->n_heads_kv * cfg->head_dim * 2;
     if ((q != q_out && overlap(q, q_bytes, q_out, q_bytes)) || (k != k_out && overlap(k, k_bytes, k_out, k_bytes)) ||
         overlap(q, q_bytes, k_out, k_bytes) || overlap(k, k_bytes, q_out, q_bytes) ||
-        overlap(q_out, q_bytes, k_out, k_bytes))
+        overlap(q_out, q_bytes, k_out, k_bytes) || overlap(positions, 12 * total, q_out, q_bytes) ||
+        overlap(positions, 12 * total, k_out, k_bytes))
         return QSA_ERR_INVALID_ARG;
     return cuda_status(launch_rope_axes(bf(q), bf(k), positions, total, s0, s1, s2, cfg->rope_base,
                                         (flags & QSA_ROPE_INTERLEAVED) != 0, (flags & QSA_ROPE_INVERSE) != 0,

@@ -502,6 +502,7 @@ qsa_status qsa_dense_attn_prefill(const qsa_config *cfg, const qsa_bf16 *q, cons
  * (below 2^(e-6), where codes are subnormal, by at most 2^(e-10)).  A row that holds an
  * infinity or a NaN gets byte 255 and zero codes and reads back as NaN.
  *   k, v   [total_q, n_heads_kv, head_dim] bf16, 16-byte aligned, not overlapping the pool
+ * The pool's arrays must not overlap one another here (QSA_ERR_INVALID_ARG).
  * A token without a page in the table, or at a negative position (L_q,s > L_k,s), is skipped
  * and flagged QSA_ERR_DEVICE_CHECK.  Two tokens of one call must not map to the same pool row
  * (their order is undefined).
@@ -539,7 +540,7 @@ qsa_status qsa_cache_read_paged(const qsa_config *cfg, int32_t format, const voi
  *   lse  [total_q, n_heads_q] fp32 natural log-sum-exp of the scaled logits, or NULL
  *   max_len_q host: a bound of every L_q,s (chooses the kernel; a wrong one costs time, and the
  *        result does not depend on it beyond rounding)
- *   o must not overlap q or the pool, nor lse the pool
+ *   o, lse and ws must overlap neither each other nor q nor the pool (QSA_ERR_INVALID_ARG)
  * fp32 softmax and accumulation, probabilities and output rounded to bf16.  E4M3 codes enter
  * the products unrounded.  A row without a visible key (a negative position, an empty cache)
  * gets o = 0, lse = -inf.  Cache memory at positions behind a sequence's end and pages wholly
@@ -573,6 +574,7 @@ qsa_status qsa_chunk_attn_paged(const qsa_config *cfg, const qsa_bf16 *q, int32_
  *   positions [3, total] int32 (negative ones too);  total host: rows
  *   q, q_out [total, n_heads_q, head_dim] bf16, 16-byte aligned; q_out == q rotates in place;
  *   k, k_out [total, n_heads_kv, head_dim] likewise; q or k may be NULL (with its output)
+ * No other overlap of an output with an input or the other output (QSA_ERR_INVALID_ARG).
  * Angles in fp64, products in fp32, one rounding to bf16.
  */
 qsa_status qsa_rope_axes(const qsa_config *cfg, const qsa_bf16 *q, const qsa_bf16 *k, const int32_t *positions,
