@@ -39,6 +39,7 @@ struct AttShared {
     int ev_r0, ev_nseg;            // first row and number of rows it touches
     float red_max[2][4][2][kGrp];  // [tile parity][quad][group][head]
     float red_sum[4][2][kGrp];
+    uint32_t v_tail[kNSlot];       // paged decode: blocks of a slot of V that end behind the row's position
 };
 
 constexpr int kOffQ = kNSlot * kSlotBytes;

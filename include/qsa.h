@@ -339,7 +339,9 @@ qsa_status qsa_sparse_attn_decode(const qsa_config *cfg, const qsa_bf16 *q,
  * The batch's tiles are always spread evenly over the CTAs (pieces merged by a
  * second kernel).  Workspace: qsa_workspace_size(cfg, QSA_OP_DECODE_PAGED, batch,
  * batch, 0) bytes.  A page id out of range reads zeros and flags
- * QSA_ERR_DEVICE_CHECK.  The pages' own dense baseline uses a paged GQA cache.
+ * QSA_ERR_DEVICE_CHECK.  Cache memory at positions behind a sequence's end may hold
+ * anything (a pool as it was allocated, filled by qsa_cache_write_paged).  The pages'
+ * own dense baseline uses a paged GQA cache.
  */
 qsa_status qsa_sparse_attn_decode_paged(const qsa_config *cfg, const qsa_bf16 *q, const qsa_bf16 *k_pages,
                                         const qsa_bf16 *v_pages, int64_t num_pages, int32_t page_size,
