@@ -568,9 +568,10 @@ size_t chunk_workspace_bytes(int batch, int64_t total_q)
 }
 
 // Single tokens (max_len_q <= 1): e4m3 pages here, 403 us against 790 us of the tensor-core kernel at batch
-// 64 of 32768 cached tokens, whose warps that make bf16 of the codes are its bound; bf16 pages there
-// (646 us against 708 us, 38.5 against 43.0 us at batch 8 of 8192), but for a few tokens, where
-// its longer start counts (one of 8191: 18.2 us here, 20.3 us there).
+// 64 of 32768 cached tokens, whose warps that make bf16 of the codes are its bound; bf16 pages there, but for a few
+// tokens, where its longer start counts.  Here and there, caches not in L2: one token over 1000, 8192 or 32768 cached
+// 16.4 and 20.5, 22.5 and 26.6, 30.7 and 36.9 us; seven 22.5 and 24.6, 43.0 and 43.0, 110.6 and 102.4 us; ten 26.6 and
+// 28.7, 57.3 and 57.3, 147.5 and 135.2 us; 32 36.9 and 34.8, 127.0 and 116.7, 387 and 346 us.
 cudaError_t launch_chunk_attn(const ChunkArgs &a, cudaStream_t stream)
 {
     if (a.total_q <= 0) return cudaSuccess;
