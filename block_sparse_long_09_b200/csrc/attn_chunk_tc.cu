@@ -19,7 +19,7 @@
 // 97 % of the copy rate; e4m3 394 us against a pair's 515).  A single CTA is the faster one up to its ten tokens in
 // every case measured: 2, 4, 8 and 10 tokens over 1, 4, 16 and 32 caches of 1000, 8192 and 32768, by 7 to 26 % in
 // bf16 and 10 to 35 % in e4m3.
-// Measured: 1024 new tokens over 16384, 1.38 PFLOP/s bf16, 1.17 e4m3; 2048 over 65536, bf16, 2.8 ms,
+// Measured: 1024 new tokens over 16384, 1.38 PFLOP/s bf16, 1.10 e4m3; 2048 over 65536, bf16, 2.8 ms,
 // 1.17 PFLOP/s under the power cap (84 % of the sustained product rate).  A tile takes 2450 cycles in
 // bf16, bound by the chain S -> softmax -> O of 2300; 2900 in e4m3, where the softmax shares its
 // schedulers with the conversion (ten operations per four codes).

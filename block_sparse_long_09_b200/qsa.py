@@ -1,9 +1,10 @@
 """Python binding of libqsa.so (the C ABI declared in include/qsa.h).
 
 Argument marshalling only (the paged-cache calls' in csrc/binding.cpp, for its speed):
-every step of the QSA path runs in the library's CUDA kernels.  torch supplies device memory and the current stream.  If the
-shared library is missing this module raises at import time -- there is no
-fallback implementation.
+every step of the QSA path runs in the library's CUDA kernels.  torch supplies device
+memory and the current stream.  If the shared library is missing this module raises at
+import time, and a paged-cache call if its compiled checks are -- there is no fallback
+implementation.
 """
 from __future__ import annotations
 
@@ -511,7 +512,8 @@ def cache_write_paged(k, v, k_pages, v_pages, block_table, cu_seqlens_q, cu_seql
     """New tokens' K and V rows [total_q, 2, 256] bf16 into a paged pool [num_pages, page_size,
     2, 256], as bf16 or, for float8_e4m3fn pages, as codes with one power-of-two scale byte per
     (token, head) in k_scales, v_scales [num_pages, page_size, 2] uint8.  Token i of
-    sequence s goes to position L_k - L_q + i (cu_seqlens_k counts the new tokens)."""
+    sequence s goes to position L_k - L_q + i (cu_seqlens_k counts the new tokens).  The pool's
+    arrays share no memory."""
     st = _binding.cache_write_paged(_cfg_addr(cfg), k, v, k_pages, v_pages, block_table, k_scales, v_scales,
                                     cu_seqlens_q, cu_seqlens_k)
     if st != QSA_OK:
@@ -535,7 +537,9 @@ def chunk_attn_paged(q, k_pages, v_pages, block_table, cu_seqlens_q, cu_seqlens_
     """Dense causal attention of every sequence's new tokens (q [total_q, 24, 256], one or many
     per sequence) over its paged bf16 or e4m3 cache, which holds them already.  window > 0: a
     token sees the last `window` positions, itself included, and the first `sinks`
-    ones.  max_len_q bounds every sequence's new tokens, max_len_k (unused so far) its cache."""
+    ones.  max_len_q bounds every sequence's new tokens, max_len_k (unused so far) its cache.  With several
+    new tokens of a sequence a V value that is not finite, seen by one of them, may make a NaN of another's output
+    too, though that one does not see it."""
     st, o, lse = _binding.chunk_attn_paged(_cfg_addr(cfg), q, k_pages, v_pages, block_table, k_scales, v_scales,
                                            cu_seqlens_q, cu_seqlens_k, max_len_q, max_len_k, window, sinks, o, lse,
                                            want_lse, ws)

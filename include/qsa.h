@@ -551,7 +551,7 @@ qsa_status qsa_cache_read_paged(const qsa_config *cfg, int32_t format, const voi
  * value and flags QSA_ERR_DEVICE_CHECK.  Several new tokens of a sequence: a non-finite V value that one
  * of them sees may make a NaN of another's output too, though that one does not see it.
  * (e4m3 pages and max_len_q <= 1: q and the probabilities as fp16 relative to their row's largest,
- * the probabilities' rounding 2^-12; otherwise probabilities as bf16.)
+ * the probabilities' rounding 2^-12, |q| below 2^110; otherwise probabilities as bf16.)
  * Workspace: qsa_workspace_size(cfg, QSA_OP_CHUNK_PAGED, batch, total_q, 0) bytes (about 41 MB), 16-byte
  * aligned; calls that may overlap on the GPU need one each.  Nothing is kept in it from one call
  * to the next, and it may hold anything before.
