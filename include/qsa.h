@@ -541,7 +541,7 @@ qsa_status qsa_cache_read_paged(const qsa_config *cfg, int32_t format, const voi
  *   q    [total_q, n_heads_q, head_dim] bf16, 16-byte aligned, and so o
  *   lse  [total_q, n_heads_q] fp32 natural log-sum-exp of the scaled logits, or NULL
  *   max_len_q host: a bound of every L_q,s (chooses the kernel; a wrong one costs time, and the
- *        result does not depend on it beyond rounding)
+ *        result does not depend on it beyond rounding and what is said of non-finite V below)
  *   o, lse and ws must overlap neither each other nor q nor the pool (QSA_ERR_INVALID_ARG)
  * fp32 softmax and accumulation, probabilities and output rounded to bf16.  E4M3 codes enter
  * the products unrounded.  A row without a visible key (a negative position, an empty cache)
